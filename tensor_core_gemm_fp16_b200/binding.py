@@ -1,9 +1,10 @@
-"""ctypes binding of libtg_gemm.so (include/tg_gemm.h, include/tg_attention.h),
-argument marshalling only.
+"""ctypes binding of libtg_gemm.so (include/tg_gemm.h, include/tg_attention.h,
+include/tg_cache.h), argument marshalling only.
 
 The raw entry points keep the C names (``tg_gemm``, ``tg_gemm_ex``, ...) and
-take integers for pointers and the stream.  ``gemm`` / ``gemm_host`` are the
-torch-tensor conveniences: they check dtype, shape, contiguity and device,
+take integers for pointers and the stream.  ``gemm``, ``gemm_host``,
+``attention``, ``cache_plan``, ``cache_write``, ``tree_mask`` and
+``tree_attention`` are the torch-tensor conveniences: they check dtype, shape, contiguity and device,
 pass ``data_ptr()`` and the current stream, and raise on a non-OK status.
 Every step of the computation runs in the library's CUDA kernels; there is
 no fallback of any kind, and a missing library is an error.
@@ -13,11 +14,13 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtg_gemm.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "tg_gemm.h")
-HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "tg_attention.h")]
+HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "tg_attention.h"),
+           os.path.join(os.path.dirname(HERE), "include", "tg_cache.h")]
 
 TG_EPILOGUE_NONE = 0
 TG_EPILOGUE_BIAS = 1
@@ -38,6 +41,11 @@ TG_ERR_SCRATCH_LIMIT = 8
 TG_INJECT_SKIP_FIRST_LOAD = 1
 TG_ATTN_SPLIT_AUTO, TG_ATTN_SPLIT_NEVER, TG_ATTN_SPLIT_ALL = 0, 1, 2
 TG_INJECT_SKIP_STREAMK_FLAGS = 2
+TG_TYPE_FP16, TG_TYPE_BF16 = 0, 1
+TG_CACHE_MAX_BATCH = 8192
+TG_TREE_MAX_WORDS = 64
+TG_PLAN_NO_PAGES, TG_PLAN_TABLE_FULL, TG_PLAN_BAD_LENGTH = 1, 2, 4
+TG_PLAN_BAD_TOKENS, TG_PLAN_BAD_RING = 8, 16
 TG_SPLIT_AUTO = 0
 TG_SPLIT_TILES = 1
 TG_SPLIT_STREAM_K = 2
@@ -70,6 +78,24 @@ class tg_attention_options_t(ctypes.Structure):
 class tg_options_t(ctypes.Structure):
     _fields_ = [("config_id", ctypes.c_int), ("wait_limit_ns", ctypes.c_uint64),
                 ("inject", ctypes.c_int), ("group_m", ctypes.c_int), ("split", ctypes.c_int)]
+
+
+class tg_tree_attention_t(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int)] + \
+        [(n, ctypes.c_int64) for n in ("tokens", "batch", "kv_heads", "group", "head_dim")] + \
+        [("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+         ("q_head_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+         ("kv_token_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64),
+         ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "page_stride", "slot_stride",
+                                       "cache_head_stride")] + \
+        [("block_tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+         ("max_pages", ctypes.c_int64), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+         ("mask", ctypes.c_void_p), ("words", ctypes.c_int64), ("mask_stride", ctypes.c_int64),
+         ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64),
+         ("out_head_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+         ("workspace_bytes", ctypes.c_size_t), ("wait_limit_ns", ctypes.c_uint64),
+         ("inject", ctypes.c_int)]
 
 
 _lib = None
@@ -120,6 +146,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tg_attention_plan.argtypes = [i64, i64, i64, i64, i64, c_int, c_int, c_int, i64p, i64p,
                                       i64p]
     lib.tg_attention_plan.restype = c_int
+    lib.tg_cache_plan.argtypes = [vp, vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, i64, vp, vp, vp,
+                                  vp, vp, vp, vp, vp]
+    lib.tg_cache_plan.restype = c_int
+    lib.tg_cache_write.argtypes = [vp, vp] + [i64] * 5 + [vp, vp, vp] + [i64] * 5 + [vp]
+    lib.tg_cache_write.restype = c_int
+    lib.tg_tree_mask.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp]
+    lib.tg_tree_mask.restype = c_int
+    lib.tg_tree_attention.argtypes = [ctypes.POINTER(tg_tree_attention_t), vp]
+    lib.tg_tree_attention.restype = c_int
+    lib.tg_tree_attention_workspace_size.argtypes = [i64]
+    lib.tg_tree_attention_workspace_size.restype = sz
     _lib = lib
     return lib
 
@@ -354,4 +391,269 @@ def gemm_host(a, b, bias=None, epilogue=None, out=None, workspace=None, device=N
         if st != TG_OK:
             raise TgError(st, "tg_gemm_host")
         stream.synchronize()
+    return out
+
+
+# ---------------------------------------------------------------- paged cache
+
+def tg_cache_plan(lens, add, batch, starts, offsets, tokens, block_tables, table_stride, max_pages,
+                  page_size, free_pages, num_pages, ring, lens_out, ring_out, starts_out, slots,
+                  positions, status, stream=None) -> int:
+    return load().tg_cache_plan(lens, add, batch, starts, offsets, tokens, block_tables,
+                                table_stride, max_pages, page_size, free_pages, num_pages, ring,
+                                lens_out, ring_out, starts_out, slots, positions, status, stream)
+
+
+def tg_cache_write(k, v, tokens, heads, head_dim, token_stride, head_stride, slots, k_cache,
+                   v_cache, num_pages, page_size, page_stride, slot_stride, cache_head_stride,
+                   stream=None) -> int:
+    return load().tg_cache_write(k, v, tokens, heads, head_dim, token_stride, head_stride, slots,
+                                 k_cache, v_cache, num_pages, page_size, page_stride, slot_stride,
+                                 cache_head_stride, stream)
+
+
+def tg_tree_mask(parents, tokens, starts, batch, words, mask, depth, stream=None) -> int:
+    return load().tg_tree_mask(parents, tokens, starts, batch, words, mask, depth, stream)
+
+
+def tg_tree_attention(args: tg_tree_attention_t, stream=None) -> int:
+    return load().tg_tree_attention(ctypes.byref(args), stream)
+
+
+def tg_tree_attention_workspace_size(head_dim: int) -> int:
+    return load().tg_tree_attention_workspace_size(head_dim)
+
+
+class CachePlan(NamedTuple):
+    """What ``cache_plan`` writes (see tg_cache_plan): lengths, ring and packing after the call,
+    each token's slot and position, and the status word (0, or TG_PLAN_* bits)."""
+    lens: "torch.Tensor"        # (B,) int32
+    ring: "torch.Tensor"        # (2,) int32
+    starts: "torch.Tensor"      # (B + 1,) int32
+    slots: "torch.Tensor"       # (tokens,) int64
+    positions: "torch.Tensor"   # (tokens,) int32
+    status: "torch.Tensor"      # (1,) int32
+
+
+def _check(name, t, dtype, shape, device):
+    """An index tensor: its type, shape (None: any extent), device and contiguity."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _table(name, t, rows, device):
+    """An int32 table whose rows are contiguous; returns its row stride."""
+    if t.dtype.itemsize != 4 or t.dtype.is_floating_point:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must have shape ({rows}, n), got {tuple(t.shape)}")
+    stride = t.stride(0) if rows > 1 else max(t.shape[1], 1)
+    if (t.shape[1] > 1 and t.stride(1) != 1) or stride < t.shape[1]:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return stride
+
+
+def _rows(name, t, dtype, heads, dim, device):
+    """A (tokens, heads, dim) tensor whose last dimension is contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+
+
+def _caches(k_cache, v_cache, dtype, device):
+    """Both caches: (pages, page size, heads, dim) tensors of the same shape and strides."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be (pages, page size, heads, dim) with a contiguous "
+                             "last dimension")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+
+
+def _call(torch, device, what, f, *args):
+    """Call a raw entry point on the device's current stream; raise on a non-OK status."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, stream)
+    if st != TG_OK:
+        raise TgError(st, what)
+
+
+def _cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def cache_plan(lens, add, ring, free_pages, block_tables, page_size, tokens, *, starts=None,
+               offsets=None, out=None):
+    """Pages, block-table entries, slots and positions for a change of the requests' lengths, on
+    the GPU through tg_cache_plan.
+
+    lens, add: (B,) int32, tokens in the cache and tokens to append (negative: to drop);
+    free_pages: (num_pages,) int32 ring of free pages with ring = (head, count); block_tables:
+    (B, max_pages) int32, extended in place; tokens: rows of the slot map.  starts (B + 1,) and
+    offsets (tokens,) int32 pick the kept ones of a packed batch of drafted tokens; without
+    them request b's max(add[b], 0) tokens are packed in order.  Returns a CachePlan, ``out``
+    (its six tensors) if given; with ``starts`` given, its starts are a copy.
+    """
+    import torch
+    dev = _cuda("lens", lens)
+    B, i32 = lens.shape[0] if lens.dim() else 0, torch.int32
+    for name, t, n in (("lens", lens, B), ("add", add, B), ("ring", ring, 2),
+                       ("free_pages", free_pages, None), ("starts", starts, B + 1),
+                       ("offsets", offsets, tokens)):
+        if t is not None:
+            _check(name, t, i32, (n,), dev)
+    stride = _table("block_tables", block_tables, B, dev)
+    if out is None:
+        def new(n):
+            return torch.empty(n, dtype=i32, device=dev)
+        out = CachePlan(new(B), new(2), new(B + 1),
+                        torch.empty(tokens, dtype=torch.int64, device=dev), new(tokens), new(1))
+    else:
+        out = CachePlan(*out)
+        for name, t, n in (("out.lens", out.lens, B), ("out.ring", out.ring, 2),
+                           ("out.starts", out.starts, B + 1),
+                           ("out.positions", out.positions, tokens), ("out.status", out.status, 1)):
+            _check(name, t, i32, (n,), dev)
+        _check("out.slots", out.slots, torch.int64, (tokens,), dev)
+    _call(torch, dev, "tg_cache_plan", load().tg_cache_plan, lens.data_ptr(), add.data_ptr(), B,
+          starts.data_ptr() if starts is not None else None,
+          offsets.data_ptr() if offsets is not None else None, tokens, block_tables.data_ptr(),
+          stride, block_tables.shape[1], page_size, free_pages.data_ptr(), free_pages.shape[0],
+          ring.data_ptr(), out.lens.data_ptr(), out.ring.data_ptr(), out.starts.data_ptr(),
+          out.slots.data_ptr(), out.positions.data_ptr(), out.status.data_ptr())
+    return out
+
+
+def cache_write(k, v, slots, k_cache, v_cache):
+    """k_cache[slots] = k, v_cache[slots] = v on the GPU through tg_cache_write.
+
+    k, v: (tokens, heads, D), any 16-bit type, same strides (slices of a fused projection will
+    do); slots: (tokens,) int64, -1 skips a token; caches: (pages, page size, heads, D), D 64 or
+    128, any strides with a contiguous last dimension.  Returns the caches.
+    """
+    import torch
+    dev = _cuda("k", k)
+    if k.dtype.itemsize != 2:
+        raise TypeError(f"k must have a 16-bit type, got {k.dtype}")
+    _caches(k_cache, v_cache, k.dtype, dev)
+    pages, page, heads, dim = k_cache.shape
+    _rows("k", k, k.dtype, heads, dim, dev)
+    _rows("v", v, k.dtype, heads, dim, dev)
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    _check("slots", slots, torch.int64, (k.shape[0],), dev)
+    _call(torch, dev, "tg_cache_write", load().tg_cache_write, k.data_ptr(), v.data_ptr(),
+          k.shape[0], heads, dim, k.stride(0), k.stride(1), slots.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), pages, page, k_cache.stride(0), k_cache.stride(1),
+          k_cache.stride(2))
+    return k_cache, v_cache
+
+
+def tree_mask(parents, starts, words, out=None):
+    """Ancestor masks and depths of drafted token trees on the GPU through tg_tree_mask.
+
+    parents: (tokens,) int32, index of a token's parent among its request's tokens or -1;
+    starts: (B + 1,) int32.  Returns (mask, depth): (tokens, words) and (tokens,) int32, ``out``
+    if given.
+    """
+    import torch
+    dev = _cuda("parents", parents)
+    n, i32 = parents.shape[0] if parents.dim() else 0, torch.int32
+    _check("parents", parents, i32, (n,), dev)
+    _check("starts", starts, i32, (None,), dev)
+    if starts.shape[0] < 1:
+        raise ValueError("starts must have shape (batch + 1,)")
+    if out is None:
+        out = (torch.empty((n, max(words, 0)), dtype=i32, device=dev),
+               torch.empty(n, dtype=i32, device=dev))
+    else:
+        _check("out[0]", out[0], i32, (n, words), dev)
+        _check("out[1]", out[1], i32, (n,), dev)
+    _call(torch, dev, "tg_tree_mask", load().tg_tree_mask, parents.data_ptr(), n,
+          starts.data_ptr(), starts.shape[0] - 1, words, out[0].data_ptr(), out[1].data_ptr())
+    return out
+
+
+def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=None, scale=0.0,
+                   out=None, *, workspace=None, wait_limit_ns=0, inject=0):
+    """Attention of drafted tokens over a paged cache and over one another on the GPU through
+    tg_tree_attention.
+
+    q: (tokens, heads, D), k and v: (tokens, kv_heads, D), fp16 or bf16, D 64 or 128, heads a
+    multiple of kv_heads; caches: (pages, page size, kv_heads, D); block_tables: (B, max_pages)
+    int32; lens: (B,) int32 cached tokens; starts: (B + 1,) int32 packing of the rows; mask:
+    (tokens, words) int32 from tree_mask, None: a token sees those of its request up to itself
+    (one token: decoding).  scale 0 means 1/sqrt(D).  workspace: uint8 tensor of at least
+    tg_tree_attention_workspace_size(D) bytes, allocated if None; calls that may overlap need
+    one each.  Returns ``out`` (allocated if None; rows outside every request are left as they
+    are).
+    """
+    import torch
+    dev, dt = _cuda("q", q), q.dtype
+    if dt != torch.float16 and dt != torch.bfloat16:
+        raise TypeError(f"q must be float16 or bfloat16, got {dt}")
+    _caches(k_cache, v_cache, dt, dev)
+    pages, page, kv_heads, dim = k_cache.shape
+    if q.dim() != 3 or kv_heads < 1 or q.shape[1] % kv_heads:
+        raise ValueError(f"q must have shape (tokens, a multiple of {kv_heads}, {dim}), got "
+                         f"{tuple(q.shape)}")
+    n, heads = q.shape[0], q.shape[1]
+    _rows("q", q, dt, heads, dim, dev)
+    _rows("k", k, dt, kv_heads, dim, dev)
+    _rows("v", v, dt, kv_heads, dim, dev)
+    if k.shape[0] != n or v.shape[0] != n or (n and k.stride() != v.stride()):
+        raise ValueError("q, k and v must have the same number of rows, k and v the same strides")
+    B = lens.shape[0] if lens.dim() else 0
+    _check("lens", lens, torch.int32, (B,), dev)
+    _check("starts", starts, torch.int32, (B + 1,), dev)
+    stride = _table("block_tables", block_tables, B, dev)
+    words = mask_stride = 0
+    if mask is not None:
+        mask_stride, words = _table("mask", mask, n, dev), mask.shape[1]
+        if words < 1:
+            raise ValueError("mask must have at least one word")
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=dt, device=dev)
+    else:
+        _rows("out", out, dt, heads, dim, dev)
+        if out.shape[0] != n:
+            raise ValueError(f"out must have shape {(n, heads, dim)}")
+    if workspace is None:
+        workspace = torch.empty(tg_tree_attention_workspace_size(dim), dtype=torch.uint8,
+                                device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    args = tg_tree_attention_t(
+        TG_TYPE_BF16 if dt == torch.bfloat16 else TG_TYPE_FP16, n, B, kv_heads, heads // kv_heads,
+        dim, scale, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(),
+        k.stride(0), k.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
+        k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), block_tables.data_ptr(), stride,
+        block_tables.shape[1], lens.data_ptr(), starts.data_ptr(),
+        mask.data_ptr() if mask is not None else None, words, mask_stride, out.data_ptr(),
+        out.stride(0), out.stride(1), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), wait_limit_ns, inject)
+    _call(torch, dev, "tg_tree_attention", load().tg_tree_attention, args)
     return out

@@ -66,6 +66,7 @@
 #include <utility>
 
 #include "tg_attention.h"
+#include "tg_attn.cuh"
 #include "tg_internal.h"
 #include "tg_ptx.cuh"
 
@@ -142,79 +143,6 @@ struct AttnShape {
     static_assert(kDynamicBytes <= 232448, "shared-memory budget");
 };
 
-// Instruction descriptor for kind::f16 with fp32 D and both operands K-major
-// (S = Q K^T: rows of Q and of K are contiguous along the head dimension).
-__host__ __device__ constexpr uint32_t idesc_f16_f32_kk(int m, int n)
-{
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// D (TMEM) += A (TMEM: 128 lanes x 16 fp16, two per 32-bit column) x B (shared
-// memory descriptor).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst_smem, const CUtensorMap *tm,
-                                            uint64_t *bar, int32_t x, int32_t y, int32_t z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst_smem),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ float rcp(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// Two fp32 values in one 64-bit register, and the packed f32x2 arithmetic of
-// sm_100 (one instruction for both halves).
-__device__ __forceinline__ uint64_t f2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void f2split(uint64_t v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // 2^x for two values on the FMA pipe, so that part of the softmax's
 // exponentials leave the SFU (fit_exp2.py fits R and checks this sequence):
 // x = n + r with n = round(x), r in [-1/2, 1/2]; R(r) = 1 + c1 r + c2 r^2 +
@@ -228,20 +156,6 @@ constexpr float kExp2C1 = 6.932827830e-01f;
 constexpr float kExp2C2 = 2.422083467e-01f;
 constexpr float kExp2C3 = 5.500787124e-02f;
 constexpr float kExp2Round = 12582912.0f;   // 1.5 * 2^23
-
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float min_nan(float a, float b)
-{
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 __device__ __forceinline__ uint64_t exp2_fma2(float x0, float x1)
 {
@@ -257,33 +171,6 @@ __device__ __forceinline__ uint64_t exp2_fma2(float x0, float x1)
     f2split(p2, q0, q1);
     return f2(__uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23)),
               __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23)));
-}
-
-// 16 consecutive 32-bit TMEM columns of this thread's lane from r (the
-// 16-column form of tmem_st_32x32b_x32).
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
-{
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&h);
 }
 
 // Keys visible to query tile (pair qp, tile t): all key tiles, or with the

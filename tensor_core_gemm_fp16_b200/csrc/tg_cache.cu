@@ -1,0 +1,539 @@
+// tg_cache.cu -- the small operators of include/tg_cache.h for sm_100a: block
+// tables and slot maps (tg_cache_plan), keys and values into pages
+// (tg_cache_write), ancestor masks (tg_tree_mask).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "tg_cache.h"
+#include "tg_cache_internal.h"
+#include "tg_internal.h"
+
+namespace tgc {
+
+// ---------------------------------------------------------------- tg_cache_plan
+// With have = ceil(len / P), want = ceil((len + add) / P), grow = max(want - have, 0),
+// drop = max(have - want, 0) and exclusive prefix sums G, D over the requests:
+//   table[b][have + i] = free[(head + G_b + i) mod cap]             i < grow_b
+//   free[(head + count + D_b + i) mod cap] = table[b][want + i]     i < drop_b
+//   slot of token p = page(p / P) * P + p mod P
+// The taken and the given-back ring entries never overlap (count + sum of drop
+// <= cap is checked), and a token's page is taken from the ring itself where
+// its table entry is new, so nothing a CTA reads is written by another: every
+// CTA makes the sums over all requests for itself (at most 8192, from L2) and
+// then takes its share of the pages and tokens; no CTA waits for another.
+// Bound by latency: launch, two rounds of loads, one scan.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanParams {
+    const int32_t *lens, *add, *starts, *offsets, *ring;
+    int32_t *tables, *free_pages, *lens_out, *ring_out, *starts_out, *positions, *status;
+    int64_t *slots;
+    int64_t table_stride, max_pages, num_pages;
+    int batch, tokens, page_shift;
+};
+
+struct Sums {
+    int64_t grow, drop, toks;
+};
+
+__device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b)
+{
+    return {a.grow + b.grow, a.drop + b.drop, a.toks + b.toks};
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums &a, int d)
+{
+    return {__shfl_up_sync(0xffffffffu, a.grow, d), __shfl_up_sync(0xffffffffu, a.drop, d),
+            __shfl_up_sync(0xffffffffu, a.toks, d)};
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t len, int shift)
+{
+    return (len + (int64_t(1) << shift) - 1) >> shift;
+}
+
+__device__ __forceinline__ int32_t saturate(int64_t v)
+{
+    return v > 0x7fffffff ? 0x7fffffff : static_cast<int32_t>(v);
+}
+
+// Last index i in [0, n) with a[i] <= v, for ascending a with a[0] <= v.
+__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p)
+{
+    extern __shared__ int32_t smem[];
+    const int B = p.batch;
+    int32_t *s_grow = smem;             // exclusive prefixes, [B]
+    int32_t *s_drop = s_grow + B;
+    int32_t *s_start = s_drop + B;      // [B + 1]
+    __shared__ Sums s_warp[kPlanWarps + 1];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+
+    const int64_t head = p.ring[0], count = p.ring[1];
+    int bad = 0;
+    if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages)
+        bad |= TG_PLAN_BAD_RING;
+    Sums mine{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const int64_t len = p.lens[b], after = len + p.add[b];
+        if (len < 0 || after < 0) bad |= TG_PLAN_BAD_LENGTH;
+        const int64_t have = pages_of(len < 0 ? 0 : len, p.page_shift);
+        const int64_t want = pages_of(after < 0 ? 0 : after, p.page_shift);
+        if (have > p.max_pages || want > p.max_pages) bad |= TG_PLAN_TABLE_FULL;
+        mine.grow += want > have ? want - have : 0;
+        mine.drop += have > want ? have - want : 0;
+        if (p.starts) {
+            const int32_t s = p.starts[b], e = p.starts[b + 1];
+            if (s < 0 || e < s || e > p.tokens) bad |= TG_PLAN_BAD_TOKENS;
+            s_start[b] = s;
+            if (b == B - 1) s_start[B] = e;
+        } else {
+            mine.toks += after > len ? after - len : 0;
+        }
+    }
+    // Inclusive scan over the threads.
+    Sums incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sums o = shfl_up(incl, d);
+        if (lane >= d) incl = incl + o;
+    }
+    if (lane == 31) s_warp[warp + 1] = incl;
+    if (tid == 0) s_warp[0] = {0, 0, 0};
+    __syncthreads();
+    if (warp == 0) {
+        Sums w = lane < kPlanWarps ? s_warp[lane + 1] : Sums{0, 0, 0};
+#pragma unroll
+        for (int d = 1; d < kPlanWarps; d <<= 1) {
+            const Sums o = shfl_up(w, d);
+            if (lane >= d) w = w + o;
+        }
+        __syncwarp();
+        if (lane < kPlanWarps) s_warp[lane + 1] = w;
+    }
+    __syncthreads();
+    const Sums total = s_warp[kPlanWarps];
+    if (total.grow > count) bad |= TG_PLAN_NO_PAGES;
+    if (count + total.drop > p.num_pages) bad |= TG_PLAN_BAD_RING;
+    if (!p.starts && total.toks > p.tokens) bad |= TG_PLAN_BAD_TOKENS;
+
+    Sums run = s_warp[warp] + incl;   // exclusive: this thread's own sums taken off again
+    run = {run.grow - mine.grow, run.drop - mine.drop, run.toks - mine.toks};
+    for (int b = b0; b < b1; ++b) {
+        const int64_t len = p.lens[b], after = len + p.add[b];
+        const int64_t have = pages_of(len < 0 ? 0 : len, p.page_shift);
+        const int64_t want = pages_of(after < 0 ? 0 : after, p.page_shift);
+        s_grow[b] = saturate(run.grow);
+        s_drop[b] = saturate(run.drop);
+        run.grow += want > have ? want - have : 0;
+        run.drop += have > want ? have - want : 0;
+        if (!p.starts) {
+            s_start[b] = saturate(run.toks);
+            run.toks += after > len ? after - len : 0;
+            if (b == B - 1) s_start[B] = saturate(run.toks);
+        }
+    }
+    if (B == 0 && tid == 0) s_start[0] = p.starts ? p.starts[0] : 0;
+    // Which bits any thread has seen (the barrier also publishes the prefixes).
+    int status = 0;
+#pragma unroll
+    for (int bit = 1; bit <= TG_PLAN_BAD_RING; bit <<= 1)
+        if (__syncthreads_or(bad & bit)) status |= bit;
+    const bool fine = status == 0;
+
+    const int64_t t0 = blockIdx.x * int64_t(kPlanThreads) + tid;
+    const int64_t stride = int64_t(gridDim.x) * kPlanThreads;
+    for (int64_t b = t0; b < B; b += stride)
+        p.lens_out[b] = p.lens[b] + (fine ? p.add[b] : 0);
+    if (p.starts_out)
+        for (int64_t b = t0; b <= B; b += stride) p.starts_out[b] = s_start[b];
+    if (t0 == 0) {
+        p.status[0] = status;
+        p.ring_out[0] =
+            static_cast<int32_t>(fine ? (head + total.grow) % p.num_pages : head);
+        p.ring_out[1] = static_cast<int32_t>(fine ? count - total.grow + total.drop : count);
+    }
+    if (fine && B > 0) {
+        for (int64_t i = t0; i < total.grow; i += stride) {
+            const int b = last_at_most(s_grow, B, static_cast<int32_t>(i));
+            const int64_t col = pages_of(p.lens[b], p.page_shift) + (i - s_grow[b]);
+            p.tables[b * p.table_stride + col] = p.free_pages[(head + i) % p.num_pages];
+        }
+        for (int64_t i = t0; i < total.drop; i += stride) {
+            const int b = last_at_most(s_drop, B, static_cast<int32_t>(i));
+            const int64_t col =
+                pages_of(int64_t(p.lens[b]) + p.add[b], p.page_shift) + (i - s_drop[b]);
+            p.free_pages[(head + count + i) % p.num_pages] = p.tables[b * p.table_stride + col];
+        }
+    }
+    const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
+    for (int64_t i = t0; i < p.tokens; i += stride) {
+        int64_t slot = -1, pos = -1;
+        if (fine && B > 0 && i >= s_start[0] && i < s_start[B]) {
+            const int b = last_at_most(s_start, B, static_cast<int32_t>(i));
+            const int64_t off = p.offsets ? p.offsets[i] : i - s_start[b];
+            if (off >= 0 && off < p.add[b]) {
+                const int64_t len = p.lens[b];
+                pos = len + off;
+                const int64_t col = pos >> p.page_shift, have = pages_of(len, p.page_shift);
+                const int64_t page =
+                    col < have ? p.tables[b * p.table_stride + col]
+                               : p.free_pages[(head + s_grow[b] + (col - have)) % p.num_pages];
+                slot = (page << p.page_shift) + (pos & page_mask);
+            }
+        }
+        p.slots[i] = slot;
+        p.positions[i] = static_cast<int32_t>(pos);
+    }
+}
+
+// ---------------------------------------------------------------- tg_cache_write
+// A copy, bound by HBM (keys and values read once, written once).  A warp takes
+// a token: its keys' and values' 16-byte pieces, up to 8 per lane in flight
+// together; the pieces of a head are contiguous on both sides.
+constexpr int kWriteThreads = 256;
+constexpr int kWriteUnroll = 8;
+
+struct WriteParams {
+    const uint4 *k, *v;
+    uint4 *kc, *vc;
+    const int64_t *slots;
+    int64_t tokens, num_slots;
+    int64_t token_stride, head_stride;                      // in 16-byte pieces
+    int64_t page_stride, slot_stride, cache_head_stride;    // in 16-byte pieces
+    int page_shift, dim_shift;                              // log2(page size), log2(head_dim / 8)
+    int pieces;                                             // 2 * heads * head_dim / 8
+};
+
+__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = int64_t(gridDim.x) * (kWriteThreads / 32);
+    const int half = p.pieces >> 1, dmask = (1 << p.dim_shift) - 1;
+    for (int64_t t = (blockIdx.x * int64_t(kWriteThreads) + threadIdx.x) >> 5; t < p.tokens;
+         t += warps) {
+        const int64_t slot = p.slots[t];
+        if (slot < 0 || slot >= p.num_slots) continue;
+        const int64_t src0 = t * p.token_stride;
+        const int64_t dst0 = (slot >> p.page_shift) * p.page_stride +
+                             (slot & ((int64_t(1) << p.page_shift) - 1)) * p.slot_stride;
+        for (int c0 = lane; c0 < p.pieces; c0 += 32 * kWriteUnroll) {
+            uint4 x[kWriteUnroll];
+#pragma unroll
+            for (int u = 0; u < kWriteUnroll; ++u) {
+                const int c = c0 + 32 * u;
+                if (c < p.pieces) {
+                    const int e = c < half ? c : c - half;
+                    const int64_t off = src0 + (e >> p.dim_shift) * p.head_stride + (e & dmask);
+                    x[u] = __ldg((c < half ? p.k : p.v) + off);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kWriteUnroll; ++u) {
+                const int c = c0 + 32 * u;
+                if (c < p.pieces) {
+                    const int e = c < half ? c : c - half;
+                    const int64_t off =
+                        dst0 + (e >> p.dim_shift) * p.cache_head_stride + (e & dmask);
+                    (c < half ? p.kc : p.vc)[off] = x[u];
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- tg_tree_mask
+// A warp takes a token and walks from it to the root through the request's
+// parents in shared memory; lane w (and w + 32) collects the bits of mask word
+// w.  A parent is below its child, so a walk ends after at most 32 * words
+// steps.  Bound by the latency of the walk's shared-memory loads.
+constexpr int kMaskThreads = 256;
+constexpr int kMaskTokens = 32;      // tokens of one CTA
+
+struct MaskParams {
+    const int32_t *parents, *starts;
+    int32_t *mask, *depth;
+    int tokens, batch, words;
+};
+
+__device__ __forceinline__ int clamp_row(int v, int tokens)
+{
+    return v < 0 ? 0 : (v > tokens ? tokens : v);
+}
+
+__global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const MaskParams p)
+{
+    extern __shared__ int16_t s_up[];    // parent of each token; kBad: not a token of a tree
+    constexpr int16_t kBad = -2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int W = p.words;
+    const int b = blockIdx.x / W, part = blockIdx.x % W;
+    if (b == p.batch) {
+        // Rows before the first request and behind the last.
+        const int first = clamp_row(p.starts[0], p.tokens);
+        const int last = clamp_row(p.starts[p.batch], p.tokens);
+        for (int64_t i = tid; i < p.tokens; i += kMaskThreads) {
+            if (i >= first && i < last) continue;
+            p.depth[i] = -1;
+            for (int w = 0; w < W; ++w) p.mask[i * W + w] = 0;
+        }
+        return;
+    }
+    const int row0 = clamp_row(p.starts[b], p.tokens);
+    const int n = clamp_row(p.starts[b + 1], p.tokens) - row0;
+    const int n_tree = min(n, 32 * W);
+    const int i0 = part * kMaskTokens;
+    // Tokens past the mask's width (the last CTA of the request).
+    if (part == W - 1)
+        for (int64_t i = n_tree + tid; i < n; i += kMaskThreads) {
+            p.depth[row0 + i] = -1;
+            for (int w = 0; w < W; ++w) p.mask[(row0 + i) * W + w] = 0;
+        }
+    const int i1 = min(i0 + kMaskTokens, n_tree);
+    if (i0 >= i1) return;
+    for (int i = tid; i < i1; i += kMaskThreads) {
+        const int u = p.parents[row0 + i];
+        s_up[i] = u >= -1 && u < i ? static_cast<int16_t>(u) : kBad;
+    }
+    __syncthreads();
+    for (int i = i0 + warp; i < i1; i += kMaskThreads / 32) {
+        uint32_t lo = 0, hi = 0;     // words `lane` and `lane + 32`
+        int depth = -1, a = i;
+        while (a >= 0) {
+            const uint32_t bit = 1u << (a & 31);
+            if ((a >> 5) == lane) lo |= bit;
+            if ((a >> 5) == lane + 32) hi |= bit;
+            ++depth;
+            a = s_up[a];
+        }
+        if (a == kBad) {
+            lo = hi = 0;
+            depth = -1;
+        }
+        int32_t *out = p.mask + int64_t(row0 + i) * W;
+        if (lane < W) out[lane] = static_cast<int32_t>(lo);
+        if (lane + 32 < W) out[lane + 32] = static_cast<int32_t>(hi);
+        if (lane == 0) p.depth[row0 + i] = depth;
+    }
+}
+
+}  // namespace tgc
+
+namespace {
+
+using namespace tgc;
+
+int grid_for(int64_t items, int per_cta, int num_sms, int ctas_per_sm)
+{
+    const int64_t want = (items + per_cta - 1) / per_cta;
+    const int64_t most = static_cast<int64_t>(num_sms) * ctas_per_sm;
+    return static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
+}
+
+}  // namespace
+
+extern "C" {
+
+tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch,
+                          const int32_t *starts, const int32_t *offsets, int64_t tokens,
+                          int32_t *block_tables, int64_t table_stride, int64_t max_pages,
+                          int64_t page_size, int32_t *free_pages, int64_t num_pages,
+                          const int32_t *ring, int32_t *lens_out, int32_t *ring_out,
+                          int32_t *starts_out, int64_t *slots, int32_t *positions,
+                          int32_t *status, void *stream)
+{
+    const int shift = page_shift_of(page_size);
+    if (batch < 0 || batch > TG_CACHE_MAX_BATCH || tokens < 0 || tokens >= kInt32 || shift < 0 ||
+        max_pages < 0 || max_pages >= kInt32 || table_stride < max_pages ||
+        table_stride >= kInt32 || num_pages < 1 || num_pages >= kInt32 || (offsets && !starts))
+        return TG_ERR_INVALID_ARG;
+    if (!ring || !ring_out || !status || !free_pages || (batch > 0 && (!lens || !add || !lens_out)) ||
+        (batch > 0 && max_pages > 0 && !block_tables) || (tokens > 0 && (!slots || !positions)))
+        return TG_ERR_INVALID_ARG;
+    const void *word[] = {lens,       add,  starts,   offsets,  block_tables, free_pages,
+                          ring,       lens_out, ring_out, starts_out, positions, status};
+    for (const void *q : word)
+        if (misaligned(q, 4)) return TG_ERR_MISALIGNED;
+    if (misaligned(slots, 8)) return TG_ERR_MISALIGNED;
+    const size_t nb = static_cast<size_t>(batch) * 4, nt = static_cast<size_t>(tokens) * 4;
+    const size_t table_bytes =
+        batch > 0 ? static_cast<size_t>((batch - 1) * table_stride + max_pages) * 4 : 0;
+    const Range in[] = {{lens, nb}, {add, nb}, {starts, nb + 4}, {offsets, nt}, {ring, 8}};
+    const Range out[] = {{block_tables, table_bytes},
+                         {free_pages, static_cast<size_t>(num_pages) * 4},
+                         {lens_out, nb},
+                         {ring_out, 8},
+                         {starts_out, nb + 4},
+                         {slots, 2 * nt},
+                         {positions, nt},
+                         {status, 4}};
+    for (const Range &o : out) {
+        for (const Range &i : in)
+            if (overlap(o, i)) return TG_ERR_INVALID_ARG;
+        for (const Range &o2 : out)
+            if (&o != &o2 && overlap(o, o2)) return TG_ERR_INVALID_ARG;
+    }
+    int num_sms = 0;
+    unsigned *error_word = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const tg_status_t st = tg_internal_device(&num_sms, &error_word, &encode);
+    if (st != TG_OK) return st;
+
+    tgc::PlanParams p;
+    p.lens = lens;
+    p.add = add;
+    p.starts = starts;
+    p.offsets = offsets;
+    p.ring = ring;
+    p.tables = block_tables;
+    p.free_pages = free_pages;
+    p.lens_out = lens_out;
+    p.ring_out = ring_out;
+    p.starts_out = starts_out;
+    p.positions = positions;
+    p.status = status;
+    p.slots = slots;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.batch = static_cast<int>(batch);
+    p.tokens = static_cast<int>(tokens);
+    p.page_shift = shift;
+    const int smem = static_cast<int>(3 * batch + 1) * 4;
+    // More than the default limit of shared memory (the scan's sums take some too).
+    if (smem > 47 * 1024 &&
+        cudaFuncSetAttribute(tgc::cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (3 * TG_CACHE_MAX_BATCH + 1) * 4) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    const int grid = grid_for(tokens > batch ? tokens : batch, tgc::kPlanThreads, num_sms, 1);
+    tgc::cache_plan_kernel<<<grid, tgc::kPlanThreads, smem,
+                             static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
+}
+
+tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t heads,
+                           int64_t head_dim, int64_t token_stride, int64_t head_stride,
+                           const int64_t *slots, void *k_cache, void *v_cache, int64_t num_pages,
+                           int64_t page_size, int64_t page_stride, int64_t slot_stride,
+                           int64_t cache_head_stride, void *stream)
+{
+    const int shift = page_shift_of(page_size);
+    if (tokens < 0 || heads < 0 || heads > (1 << 20) || num_pages < 0 || num_pages >= kInt32 ||
+        shift < 0 || (head_dim != 64 && head_dim != 128))
+        return TG_ERR_INVALID_ARG;
+    if (tokens >= kInt32) return TG_ERR_INVALID_ARG;
+    if (tokens == 0 || heads == 0 || num_pages == 0) return TG_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache) return TG_ERR_INVALID_ARG;
+    // Strides of dimensions with more than one element.  Rows of a cache may be
+    // interleaved with others, not with one another.
+    const Dim src_dims[] = {{tokens, token_stride}, {heads, head_stride}};
+    const Dim dst_dims[] = {
+        {num_pages, page_stride}, {page_size, slot_stride}, {heads, cache_head_stride}};
+    for (const Dim &d : src_dims)
+        if (d.n > 1 && (d.stride < 0 || d.stride >= (int64_t(1) << 40))) return TG_ERR_INVALID_ARG;
+    for (const Dim &d : dst_dims)
+        if (d.n > 1 && (d.stride < head_dim || d.stride >= (int64_t(1) << 40)))
+            return TG_ERR_INVALID_ARG;
+    for (const Dim &d : src_dims)
+        if (d.n > 1 && (d.stride & 7)) return TG_ERR_MISALIGNED;
+    for (const Dim &d : dst_dims)
+        if (d.n > 1 && (d.stride & 7)) return TG_ERR_MISALIGNED;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_cache, 16) ||
+        misaligned(v_cache, 16) || misaligned(slots, 8))
+        return TG_ERR_MISALIGNED;
+    const size_t src = extent({{tokens, token_stride}, {heads, head_stride}}, head_dim);
+    const size_t dst = extent({{num_pages, page_stride},
+                               {page_size, slot_stride},
+                               {heads, cache_head_stride}},
+                              head_dim);
+    const Range in[] = {{k, src}, {v, src}, {slots, 8 * static_cast<size_t>(tokens)}};
+    for (const Range &i : in)
+        if (overlap(i, {k_cache, dst}) || overlap(i, {v_cache, dst})) return TG_ERR_INVALID_ARG;
+    // The two caches may be interleaved (slices of one tensor), not the same.
+    if (k_cache == v_cache) return TG_ERR_INVALID_ARG;
+    int num_sms = 0;
+    unsigned *error_word = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const tg_status_t st = tg_internal_device(&num_sms, &error_word, &encode);
+    if (st != TG_OK) return st;
+
+    tgc::WriteParams p;
+    p.k = static_cast<const uint4 *>(k);
+    p.v = static_cast<const uint4 *>(v);
+    p.kc = static_cast<uint4 *>(k_cache);
+    p.vc = static_cast<uint4 *>(v_cache);
+    p.slots = slots;
+    p.tokens = tokens;
+    p.num_slots = num_pages << shift;
+    p.token_stride = token_stride / 8;
+    p.head_stride = head_stride / 8;
+    p.page_stride = page_stride / 8;
+    p.slot_stride = slot_stride / 8;
+    p.cache_head_stride = cache_head_stride / 8;
+    p.page_shift = shift;
+    p.dim_shift = head_dim == 64 ? 3 : 4;
+    p.pieces = static_cast<int>(2 * heads * (head_dim / 8));
+    const int grid = grid_for(tokens, tgc::kWriteThreads / 32, num_sms, 8);
+    tgc::cache_write_kernel<<<grid, tgc::kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
+}
+
+tg_status_t tg_tree_mask(const int32_t *parents, int64_t tokens, const int32_t *starts,
+                         int64_t batch, int64_t words, int32_t *mask, int32_t *depth,
+                         void *stream)
+{
+    if (tokens < 0 || tokens >= kInt32 || batch < 0 || words < 1 || words > TG_TREE_MAX_WORDS ||
+        (batch + 1) * words >= kInt32)
+        return TG_ERR_INVALID_ARG;
+    if (tokens == 0) return TG_OK;
+    if (!parents || !starts || !mask || !depth) return TG_ERR_INVALID_ARG;
+    if (misaligned(parents, 4) || misaligned(starts, 4) || misaligned(mask, 4) ||
+        misaligned(depth, 4))
+        return TG_ERR_MISALIGNED;
+    const size_t nt = static_cast<size_t>(tokens) * 4;
+    const Range in[] = {{parents, nt}, {starts, static_cast<size_t>(batch + 1) * 4}};
+    const Range out[] = {{mask, nt * static_cast<size_t>(words)}, {depth, nt}};
+    for (const Range &o : out)
+        for (const Range &i : in)
+            if (overlap(o, i)) return TG_ERR_INVALID_ARG;
+    if (overlap(out[0], out[1])) return TG_ERR_INVALID_ARG;
+    int num_sms = 0;
+    unsigned *error_word = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const tg_status_t st = tg_internal_device(&num_sms, &error_word, &encode);
+    if (st != TG_OK) return st;
+
+    tgc::MaskParams p;
+    p.parents = parents;
+    p.starts = starts;
+    p.mask = mask;
+    p.depth = depth;
+    p.tokens = static_cast<int>(tokens);
+    p.batch = static_cast<int>(batch);
+    p.words = static_cast<int>(words);
+    const int grid = static_cast<int>(batch * words + 1);
+    tgc::tree_mask_kernel<<<grid, tgc::kMaskThreads, static_cast<size_t>(words) * 64,
+                            static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,1147 @@
+// tg_tree_attention.cu -- attention of drafted token trees (or single tokens)
+// over a paged cache for sm_100a (tcgen05 + TMEM + TMA); tg_tree_attention of
+// include/tg_cache.h.
+//
+// Rows.  The query heads that share a key head see the same keys, so a tile of
+// 128 query rows holds (token, head) pairs of one request and key head:
+// 128 / group tokens with all their heads, one TMA box of the packed queries.
+// Keys come in tiles of 128: first the request's cached tokens, page by page
+// (a TMA box each, the block table's entry as a coordinate), then its drafted
+// tokens from their dense tensor.
+//
+// Work division.  A unit is (request, key head, pair of query tiles); its
+// length is the request's number of key tiles.  Only the device knows the
+// lengths, so each CTA sums them up itself and takes an equal share of all key
+// tiles, wherever units begin and end: the last unit of a CTA's share may go
+// on in the next CTA.  A unit that lies in one CTA is finished there; the
+// parts of a divided one leave their unnormalised output, maxima and sums in
+// the workspace, and a second kernel joins them in the CTAs' order.
+//
+// One CTA per SM, ten warps:
+//   warps 0-3, 4-7  two softmax groups, thread r of a group owns query row r
+//                   (TMEM lane r).  A unit with two query tiles gives one to
+//                   each group, both over all key tiles; a unit with one gives
+//                   it to both, one group taking the even key tiles and the
+//                   other the odd ones, each with its own maximum, sum and
+//                   output, joined at the end in tensor memory.  Either way
+//                   one group's exponentials run beside the other's products.
+//   warp 8          TMA producer: queries, and keys and values through one
+//                   ring in the order in which the products need them.
+//   warp 9          TMEM allocator and MMA issuer.
+// Step i belongs to group t = i mod 2.  The issuer's order is S_0 S_1, then
+// P_i V, S_i+2 for i = 0, 1, ...; P_i (16 bits) overwrites S_i in tensor
+// memory, and S_i+2 follows P_i V in the tensor pipe's order.
+// TMEM: S_t / P_t at columns 128 t, O_t at 256 + D t.
+//
+// Masked places.  A masked score becomes -inf before the maximum.  A masked
+// key's value still enters the product with weight 0, so values that are not
+// finite there would spread: in a tile that is not wholly visible the group
+// zeroes, in shared memory, the values of rows past the end, and elements
+// that are not finite; what visible drafted tokens lose by that is added
+// back at the end from global memory (a rare path behind a flag).
+//
+// Every wait is bounded; see tg_attention.cu.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "tg_attn.cuh"
+#include "tg_cache.h"
+#include "tg_cache_internal.h"
+#include "tg_internal.h"
+
+namespace tgt {
+
+using namespace tga;
+
+constexpr int kRows = 128;         // query rows of a tile (TMEM lanes)
+constexpr int kKeys = 128;         // keys of a tile (score columns)
+constexpr int kAtom = 64;          // head-dim elements per 128-byte swizzle atom
+constexpr int kAtomBytes = 128 * 128;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kWarps = 10;
+constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOBase = 256;
+constexpr int kMaxCtas = 148;      // one per SM of a B200; the workspace's size goes by it
+
+// Error word bits (shared with the other kernels of the library).
+constexpr unsigned kErrTreeProducer = 1024u;
+constexpr unsigned kErrTreeMma = 2048u;
+constexpr unsigned kErrTreeSoftmax = 4096u;
+constexpr unsigned kErrTreeDrain = 8192u;
+constexpr unsigned kErrTreeSmem = 16384u;
+
+// What a CTA leaves for the joining kernel: the unit that begins in its share
+// and goes on behind it, and how many CTAs have a part of it (0: none).
+struct Split {
+    int b, unit, ctas, pad;
+};
+
+struct TreeParams {
+    const int32_t *lens, *starts, *tables, *mask;
+    const uint16_t *v;            // drafted values
+    uint16_t *out;
+    int64_t v_token_stride, v_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t table_stride, max_len, mask_stride;
+    int tokens, batch, kv_heads, group, tile_tokens, words, page_shift;
+    float scale_log2;             // scale * log2(e)
+    Split *split;                 // [CTAs]
+    float *part;                  // [CTAs][first, last part][query tile][D + 2][128]
+    int inject;
+    uint64_t wait_limit_ns;
+    unsigned *error_word;
+};
+
+template <int D>
+struct TreeShape {
+    static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+    static constexpr int kAtoms = D / kAtom;
+    static constexpr int kTileBytes = kAtoms * kAtomBytes;   // one 128-row tile
+    static constexpr int kStages = D == 128 ? 5 : 10;        // ring of key and value tiles
+    static constexpr int kQOff = 0;                          // two query tiles
+    static constexpr int kKVOff = 2 * kTileBytes;
+    static constexpr int kMlOff = kKVOff + kStages * kTileBytes;   // (m, l) of both groups
+    static constexpr int kBarOff = kMlOff + 2 * kRows * 8;
+    // q_full[2], q_empty[2], kv_full[], kv_empty[], s_full[2], p_full[2], o_full[2],
+    // o_free, ml_full, drain
+    static constexpr int kNumBars = 4 + 2 * kStages + 6 + 3;
+    static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
+    static constexpr int kAbortOff = kTmemSlotOff + 4;
+    static constexpr int kFlagOff = kAbortOff + 4;
+    static constexpr int kDynamicBytes = kFlagOff + 4;
+    static_assert(kDynamicBytes <= 232448, "shared-memory budget");
+    // Floats of one part of a divided unit's query tile: O (by columns), m, l.
+    static constexpr int kPartFloats = (D + 2) * kRows;
+};
+
+constexpr size_t split_bytes() { return (sizeof(Split) * kMaxCtas + 255) / 256 * 256; }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        return pack_half2(lo, hi);
+    }
+}
+
+// Instruction descriptor bits that select bf16 for A and B.
+template <bool BF16>
+constexpr uint32_t kTypeBits = BF16 ? (1u << 7) | (1u << 10) : 0u;
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const CUtensorMap *tm,
+                                            uint64_t *bar, int32_t x, int32_t y, int32_t z,
+                                            int32_t w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst_smem),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// A request: its drafted rows, cached tokens, tiles and work.
+struct Request {
+    int s0, n, ctx;      // first drafted row, drafted tokens, cached tokens
+    int ctx_tiles, nk;   // key tiles of the cache, and of all keys
+    int q_tiles, pairs;  // query tiles, and pairs of them
+    int64_t work;        // key tiles of all its units
+};
+
+__device__ __forceinline__ Request request(const TreeParams &p, int b)
+{
+    Request r;
+    int s0 = p.starts[b], s1 = p.starts[b + 1];
+    const int64_t len = p.lens[b];
+    s0 = min(max(s0, 0), p.tokens);
+    s1 = min(max(s1, s0), p.tokens);
+    r.s0 = s0;
+    r.n = s1 - s0;
+    r.ctx = static_cast<int>(len < 0 ? 0 : (len < p.max_len ? len : p.max_len));
+    r.ctx_tiles = (r.ctx + kKeys - 1) / kKeys;
+    r.nk = r.ctx_tiles + (r.n + kKeys - 1) / kKeys;
+    r.q_tiles = (r.n + p.tile_tokens - 1) / p.tile_tokens;
+    r.pairs = (r.q_tiles + 1) >> 1;
+    r.work = static_cast<int64_t>(p.kv_heads) * r.pairs * r.nk;
+    return r;
+}
+
+// The parts of units in a CTA's share, in order; every warp walks through them
+// by itself, all lanes together.
+struct Walk {
+    int64_t pos, end;    // what is left of the share, in key tiles
+    int64_t base;        // where request b's work begins
+    int b;
+    Request r;
+    // the current part: key tiles [k0, k1) of a unit
+    int unit, head, pair, k0, k1;
+    bool two;            // both query tiles of the pair exist
+
+    __device__ __forceinline__ bool next(const TreeParams &p, int lane)
+    {
+        if (pos >= end) return false;
+        if (pos >= base + r.work) {
+            base += r.work;
+            // the next request that has work
+            for (;;) {
+                const int mine = b + 1 + lane;
+                const bool has = mine < p.batch && request(p, mine).work > 0;
+                const unsigned any = __ballot_sync(0xffffffffu, has);
+                if (any) {
+                    b += __ffs(any);
+                    break;
+                }
+                b += 32;
+                if (b >= p.batch) return false;
+            }
+            r = request(p, b);
+        }
+        const int64_t rel = pos - base;
+        unit = static_cast<int>(rel / r.nk);
+        k0 = static_cast<int>(rel - static_cast<int64_t>(unit) * r.nk);
+        const int64_t left = end - pos;
+        k1 = left < r.nk - k0 ? k0 + static_cast<int>(left) : r.nk;
+        pos += k1 - k0;
+        head = unit / r.pairs;
+        pair = unit - head * r.pairs;
+        two = 2 * pair + 1 < r.q_tiles;
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == r.nk; }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmKC,
+                     const __grid_constant__ CUtensorMap tmVC,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const TreeParams p)
+{
+    using S = TreeShape<D>;
+    constexpr int NS = S::kStages;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBarOff);
+    uint64_t *q_full = bars;
+    uint64_t *q_empty = bars + 2;
+    uint64_t *kv_full = bars + 4;
+    uint64_t *kv_empty = kv_full + NS;
+    uint64_t *s_full = kv_empty + NS;    // [2]: S_t is in TMEM
+    uint64_t *p_full = s_full + 2;       // [2]: P_t is in TMEM (4 arrivals)
+    uint64_t *o_full = p_full + 2;       // [2]: O_t of the part complete
+    uint64_t *o_free = o_full + 2;       // both O read (8 arrivals)
+    uint64_t *ml_full = o_free + 1;      // both groups' m and l written (8 arrivals)
+    uint64_t *drain_bar = ml_full + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kTmemSlotOff);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbortOff);
+    volatile int *odd_values = reinterpret_cast<volatile int *>(smem + S::kFlagOff);
+    float2 *ml = reinterpret_cast<float2 *>(smem + S::kMlOff);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint64_t limit = p.wait_limit_ns;
+    const int cta = static_cast<int>(blockIdx.x);
+    grid_launch_dependents();
+
+    // The swizzled tiles need a 1024-byte aligned base (the alignment asked for
+    // above); uniform over the CTA.
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) {
+            p.split[cta] = Split{0, 0, 0, 0};
+            atomicOr(p.error_word, kErrTreeSmem);
+        }
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kNumBars; ++i) {
+            uint64_t *bar = &bars[i];
+            const uint32_t count = (bar == &p_full[0] || bar == &p_full[1]) ? 4u
+                                   : (bar == o_free || bar == ml_full)      ? 8u
+                                                                            : 1u;
+            mbar_init(bar, count);
+        }
+        *abort_flag = 0;
+        *odd_values = 0;
+        fence_mbar_init();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmKC);
+        tma_prefetch_desc(&tmVC);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc<1>(tmem_slot, kTmemCols);
+        tmem_relinquish<1>();
+    }
+
+    // Share of this CTA.  Scratch in the ring, which is not in use yet.
+    int64_t *scr = reinterpret_cast<int64_t *>(smem + S::kKVOff);
+    int64_t *scr_sum = scr, *scr_scan = scr + kWarps, *scr_base = scr + 2 * kWarps;
+    int *scr_b = reinterpret_cast<int *>(scr_base + 1);
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) mine += request(p, b).work;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if (lane == 0) scr_sum[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += scr_sum[w];
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t pos0 = min(total, cta * share);
+    const int64_t pos1 = min(total, pos0 + share);
+    if (pos0 == pos1 && threadIdx.x == 0) p.split[cta] = Split{0, 0, 0, 0};
+    int64_t before = 0;      // work of the requests before this chunk
+    for (int c0 = 0; c0 < p.batch && before < pos1 && pos0 < pos1; c0 += kThreads) {
+        const int b = c0 + threadIdx.x;
+        const Request r = b < p.batch ? request(p, b) : Request{0, 0, 0, 0, 0, 0, 0, 0};
+        int64_t incl = r.work;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) scr_scan[warp] = incl;
+        __syncthreads();
+        int64_t off = before, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) off += scr_scan[w];
+            sum += scr_scan[w];
+        }
+        const int64_t lo = off + incl - r.work, hi = off + incl;
+        if (lo <= pos0 && pos0 < hi) {
+            *scr_base = lo;
+            *scr_b = b;
+        }
+        if (lo < pos1 && pos1 <= hi) {
+            // The unit that holds the share's last key tile.
+            const int64_t u = (pos1 - 1 - lo) / r.nk;
+            const int64_t ubegin = lo + u * r.nk, uend = ubegin + r.nk;
+            const bool split = ubegin >= pos0 && uend > pos1;
+            const int ctas = split ? static_cast<int>((uend - 1) / share) - cta + 1 : 0;
+            p.split[cta] = Split{b, static_cast<int>(u), ctas, 0};
+        }
+        before += sum;
+        __syncthreads();     // scr_scan is written again
+    }
+    __syncthreads();
+    Walk walk;
+    walk.pos = pos0;
+    walk.end = pos1;
+    walk.base = 0;
+    walk.b = 0;
+    if (pos0 < pos1) {
+        walk.base = *scr_base;
+        walk.b = *scr_b;
+        walk.r = request(p, walk.b);
+    }
+    // The scratch is read before the ring's first copies land on it.
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, unsigned site) -> bool {
+        const bool ok = mbar_wait_bounded(bar, parity, abort_flag, limit, p.error_word, site);
+        return __all_sync(0xffffffffu, ok);
+    };
+
+    if (warp == kProducerWarp) {
+        uint32_t qc = 0, ic = 0;       // query tiles and ring items so far
+        bool ok = true;
+        const int shift = p.page_shift;
+        const bool small = shift < 7;                     // pages of less than a tile
+        const int per_tile = small ? kKeys >> shift : 1;  // pages of a tile
+        const int my_page = lane / S::kAtoms, my_atom = lane % S::kAtoms;
+        const uint32_t my_off = my_atom * kAtomBytes + (small ? my_page << (shift + 7) : 0);
+        while (ok && walk.next(p, lane)) {
+            const Request &r = walk.r;
+            for (int t = 0; t < (walk.two ? 2 : 1) && ok; ++t, ++qc) {
+                const uint32_t slot = qc & 1u;
+                if (qc >= 2) ok = wait_all(&q_empty[slot], ((qc >> 1) - 1) & 1, kErrTreeProducer);
+                if (!ok) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&q_full[slot],
+                                          p.group * p.tile_tokens * S::kAtoms * 128);
+                __syncwarp();
+                if (lane < S::kAtoms)
+                    tma_load_3d(sbase + S::kQOff + slot * S::kTileBytes + lane * kAtomBytes, &tmQ,
+                                &q_full[slot], lane * kAtom, walk.head * p.group,
+                                r.s0 + (2 * walk.pair + t) * p.tile_tokens);
+            }
+            const int n = walk.k1 - walk.k0;
+            const int32_t *table = p.tables + static_cast<int64_t>(walk.b) * p.table_stride;
+            // This lane's page of key tile kj of the cache (-1: none).
+            auto page_of = [&](int kj) -> int {
+                if (kj >= r.ctx_tiles || my_page >= per_tile) return -1;
+                const int pi = small ? kj * per_tile + my_page : (kj * kKeys) >> shift;
+                return (static_cast<int64_t>(pi) << shift) < r.ctx ? table[pi] : -1;
+            };
+            // Page entries outside the cache read as zeros (out of the map's range).
+            auto load = [&](int kj, int page, bool value) {
+                const uint32_t st = ic % NS;
+                const uint32_t dst = sbase + S::kKVOff + st * S::kTileBytes;
+                const bool skip = p.inject == 1 && cta == 0 && ic == 0;
+                if (kj < r.ctx_tiles) {
+                    const int left = r.ctx - kj * kKeys;
+                    const int pages =
+                        small ? min(per_tile, (left + (1 << shift) - 1) >> shift) : 1;
+                    const int rows = small ? pages << shift : kKeys;
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
+                    __syncwarp();
+                    if (my_page < pages && !skip)
+                        tma_load_4d(dst + my_off, value ? &tmVC : &tmKC, &kv_full[st],
+                                    my_atom * kAtom,
+                                    small ? 0 : (kj * kKeys) & ((1 << shift) - 1), walk.head,
+                                    page);
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], S::kTileBytes);
+                    __syncwarp();
+                    if (lane < S::kAtoms && !skip)
+                        tma_load_3d(dst + lane * kAtomBytes, value ? &tmV : &tmK, &kv_full[st],
+                                    lane * kAtom, r.s0 + (kj - r.ctx_tiles) * kKeys, walk.head);
+                }
+                ++ic;
+            };
+            // Items K_0 | K_1 V_0 | K_2 V_1 | ... | V_n-1; the next tile's page
+            // entries are fetched while the ring has no room.
+            int page_v = -1, page_k = page_of(walk.k0);
+            for (int t = 0; t < 2 * n && ok; ++t) {
+                if (ic >= NS)
+                    ok = wait_all(&kv_empty[ic % NS], (ic / NS - 1) & 1, kErrTreeProducer);
+                if (!ok) break;
+                const bool value = t == 2 * n - 1 || (t > 0 && (t & 1) == 0);
+                const int j = t == 2 * n - 1 ? n - 1 : (value ? t / 2 - 1 : (t + 1) / 2);
+                if (value) {
+                    load(walk.k0 + j, page_v, true);
+                    page_v = page_k;
+                    if (j + 2 < n) page_k = page_of(walk.k0 + j + 2);
+                } else {
+                    load(walk.k0 + j, page_k, false);
+                    if (j == 0) {
+                        page_v = page_k;
+                        if (n > 1) page_k = page_of(walk.k0 + 1);
+                    }
+                }
+            }
+        }
+        // Every copy lands before shared memory goes away (the injected test
+        // skips one load, whose barrier never completes).
+        if (lane == 0) {
+            for (uint32_t s = 0; s < 2; ++s)
+                if (qc > s && !mbar_wait_drain(&q_full[s], ((qc - 1 - s) >> 1) & 1, limit))
+                    atomicOr(p.error_word, kErrTreeDrain);
+            for (uint32_t s = 0; s < NS; ++s)
+                if (ic > s && !(p.inject == 1 && cta == 0 && s == 0 && ic <= NS) &&
+                    !mbar_wait_drain(&kv_full[s], ((ic - 1 - s) / NS) & 1, limit))
+                    atomicOr(p.error_word, kErrTreeDrain);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t kIdescS = idesc_f16_f32_kk(kRows, kKeys) | kTypeBits<BF16>;
+        constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | kTypeBits<BF16>;
+        uint32_t qc = 0, ic = 0, parts = 0;
+        uint32_t steps[2] = {0, 0};     // products P V issued, per group
+        bool ok = true, issued = false;
+        while (ok && walk.next(p, lane)) {
+            const bool two = walk.two;
+            const int n = walk.k1 - walk.k0;
+            const int N = two ? 2 * n : n;
+            auto stage_k = [&](int j) { return j == 0 ? ic : ic + 2 * j - 1; };
+            auto stage_v = [&](int j) { return j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2; };
+            // S_i = Q K^T
+            auto issue_s = [&](int i) -> bool {
+                const int t = i & 1, j = two ? i >> 1 : i;
+                const uint32_t qi = two ? qc + t : qc, qs = qi & 1u;
+                const uint32_t item = stage_k(j), st = item % NS;
+                if (!wait_all(&q_full[qs], (qi >> 1) & 1, kErrTreeMma)) return false;
+                if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeMma)) return false;
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t qa = sbase + S::kQOff + qs * S::kTileBytes;
+                    const uint32_t ka = sbase + S::kKVOff + st * S::kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kAtomBytes + (kk & 3) * 32;
+                        mma_f16_ss<1>(tmem_base + t * kKeys, smem_desc_sw128(qa + off, 16, 1024),
+                                      smem_desc_sw128(ka + off, 16, 1024), kIdescS, kk > 0);
+                    }
+                    mma_commit<1>(&s_full[t]);
+                    if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
+                    if (two ? i + 2 >= N : i + 1 == N) mma_commit<1>(&q_empty[qs]);
+                }
+                __syncwarp();
+                issued = true;
+                return true;
+            };
+            // O_t += P_i V
+            auto issue_pv = [&](int i) -> bool {
+                const int t = i & 1, j = two ? i >> 1 : i;
+                const uint32_t item = stage_v(j), st = item % NS;
+                if (i < 2 && parts > 0 && !wait_all(o_free, (parts - 1) & 1, kErrTreeMma))
+                    return false;
+                if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeMma)) return false;
+                if (!wait_all(&p_full[t], steps[t] & 1, kErrTreeMma)) return false;
+                ++steps[t];
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t va = sbase + S::kKVOff + st * S::kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_f16_ts(tmem_base + kOBase + t * D, tmem_base + t * kKeys + kk * 8,
+                                   smem_desc_sw128(va + kk * 2048, kAtomBytes, 1024), kIdescO,
+                                   (i >= 2 || kk > 0) ? 1u : 0u);
+                    if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
+                    if (i + 2 >= N) mma_commit<1>(&o_full[t]);
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = issue_s(0) && (N < 2 || issue_s(1));
+            for (int i = 0; ok && i < N; ++i) {
+                ok = issue_pv(i);
+                if (ok && i + 2 < N) ok = issue_s(i + 2);
+            }
+            qc += two ? 2 : 1;
+            ic += 2 * n;
+            ++parts;
+        }
+        if (issued && lane == 0) {
+            mma_commit<1>(drain_bar);
+            if (!mbar_wait_drain(drain_bar, 0, limit)) atomicOr(p.error_word, kErrTreeDrain);
+        }
+        __syncwarp();
+    } else {
+        const int t = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_s = t_lanes + t * kKeys;
+        const float sl2 = p.scale_log2;
+        uint32_t ic = 0, steps = 0, joins = 0;
+        uint32_t outs[2] = {0, 0};      // parts in which group 0, group 1 had steps
+        bool ok = true;
+        while (ok && walk.next(p, lane)) {
+            const Request &r = walk.r;
+            const bool two = walk.two;
+            const int n = walk.k1 - walk.k0;
+            const int N = two ? 2 * n : n;
+            const int tile = 2 * walk.pair + (two ? t : 0);
+            const int tok0 = tile * p.tile_tokens;
+            const int rows = min(p.tile_tokens, r.n - tok0) * p.group;
+            const bool act = quarter * 32 < rows;        // uniform over the warp
+            const int tl = row / p.group;
+            const int tok = tok0 + tl;                   // of the request
+            const int64_t grow = static_cast<int64_t>(r.s0) + tok;
+            const int32_t *mrow = p.mask ? p.mask + grow * p.mask_stride : nullptr;
+            float m = -INFINITY;   // running maximum of the scaled scores, log2 units
+            float l = 0.f;         // running sum of 2^(score - m)
+            for (int i = t; ok && i < N; i += 2) {
+                const int j = two ? i >> 1 : i;
+                const int kj = walk.k0 + j;
+                const bool tree = kj >= r.ctx_tiles;
+                const int key0 = (kj - r.ctx_tiles) * kKeys;       // first drafted key (tree)
+                const int lim = tree ? r.n - key0 : r.ctx - kj * kKeys;
+                const bool edge = tree || lim < kKeys;             // not wholly visible
+                if (!wait_all(&s_full[t], steps & 1, kErrTreeSoftmax)) {
+                    ok = false;
+                    break;
+                }
+                ++steps;
+                tc_fence_after_sync();
+                if (act) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_s + q * 32, s[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_wait_ld_dep(s[q]);
+                    if (edge) {
+                        // Visible columns: keys that exist, and for drafted ones
+                        // the row's mask (or, without one, keys up to its own).
+                        const int lim_row = tree && !mrow ? min(lim, tok + 1 - key0) : lim;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int v = lim_row - 32 * q;
+                            uint32_t vis = v >= 32 ? 0xffffffffu : (v <= 0 ? 0u : (1u << v) - 1u);
+                            if (tree && mrow) {
+                                const int w = (key0 >> 5) + q;
+                                vis &= row < rows && w < p.words
+                                           ? static_cast<uint32_t>(mrow[w])
+                                           : 0u;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((vis >> c) & 1u)) s[q][c] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    // The maximum keeps NaN (a NaN score makes the row NaN).
+                    float mx[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            mx[c & 7] = max_nan(mx[c & 7], __uint_as_float(s[q][c]));
+                    const float tmax = sl2 * max_nan(max_nan(max_nan(mx[0], mx[1]),
+                                                             max_nan(mx[2], mx[3])),
+                                                     max_nan(max_nan(mx[4], mx[5]),
+                                                             max_nan(mx[6], mx[7])));
+                    // Lazy rescale: m moves only when a tile raises it by more than 8.
+                    float alpha = 1.f;
+                    const bool raise = !(tmax <= m + 8.f);
+                    if (raise) {
+                        alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
+                        m = tmax;
+                    }
+                    // S_i came after P_i-2 V in the tensor pipe: O_t is at rest.
+                    if (i >= 2 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            const uint32_t t_o = t_lanes + kOBase + t * D + c * 32;
+                            tmem_ld_32x32b_x32(t_o, o);
+                            tmem_wait_ld_dep(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st_32x32b_x32(t_o, o);
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const uint64_t sl2x2 = f2(sl2, sl2), nmu2 = f2(-mu, -mu);
+                    uint64_t ps2[4] = {0, 0, 0, 0};
+                    // P takes the first 64 columns of S, two keys per column.
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t hp[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const uint64_t a2 = ffma2(f2(__uint_as_float(s[q][c]),
+                                                         __uint_as_float(s[q][c + 1])),
+                                                      sl2x2, nmu2);
+                            float a0, a1;
+                            f2split(a2, a0, a1);
+                            const float e0 = ex2(a0), e1 = ex2(a1);
+                            ps2[(c >> 1) & 3] = fadd2(ps2[(c >> 1) & 3], f2(e0, e1));
+                            hp[c >> 1] = pack2<BF16>(e0, e1);
+                        }
+                        tmem_st_32x32b_x16(t_s + q * 16, hp);
+                    }
+                    float q0, q1, q2, q3;
+                    f2split(fadd2(ps2[0], ps2[1]), q0, q1);
+                    f2split(fadd2(ps2[2], ps2[3]), q2, q3);
+                    l = fmaf(l, alpha, (q0 + q1) + (q2 + q3));
+                    tmem_wait_st();
+                }
+                if (edge && (!two || t == 0)) {
+                    // Values of this tile that no row may meet, see the head of
+                    // the file.  Thread r looks after key r.
+                    const uint32_t item = j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2;
+                    const uint32_t st = item % NS;
+                    if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeSoftmax)) {
+                        ok = false;
+                        break;
+                    }
+                    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+                    uint8_t *vrow = smem + S::kKVOff + st * S::kTileBytes + row * 128;
+                    bool odd = false;
+#pragma unroll
+                    for (int a = 0; a < S::kAtoms; ++a)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint4 *at = reinterpret_cast<uint4 *>(vrow + a * kAtomBytes +
+                                                                  (((c + row) & 7) << 4));
+                            if (row >= lim) {
+                                *at = make_uint4(0, 0, 0, 0);
+                            } else if (tree) {
+                                uint4 x = *at;
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                                bool hit = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & kExp) == kExp) {
+                                        w[e] &= 0xFFFF0000u;
+                                        hit = true;
+                                    }
+                                    if ((w[e] & (kExp << 16)) == (kExp << 16)) {
+                                        w[e] &= 0x0000FFFFu;
+                                        hit = true;
+                                    }
+                                }
+                                if (hit) {
+                                    *at = x;
+                                    odd = true;
+                                }
+                            }
+                        }
+                    if (odd) *odd_values = 1;
+                    fence_proxy_async_smem();     // the tensor core reads the tile next
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            // End of the part.  A single query tile: both groups' outputs are
+            // joined, each group doing half of the columns.
+            const int other_steps = N > 1 ? 1 : 0;     // group 1 had steps
+            if (!two || t == 0)
+                ok = wait_all(&o_full[0], outs[0] & 1, kErrTreeSoftmax);
+            if (ok && other_steps && (!two || t == 1))
+                ok = wait_all(&o_full[1], outs[1] & 1, kErrTreeSoftmax);
+            if (!ok) break;
+            ++outs[0];
+            outs[1] += other_steps;
+            float w0 = t == 0 ? 1.f : 0.f, w1 = t == 1 ? 1.f : 0.f;
+            if (!two) {
+                ml[t * kRows + row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                if (!wait_all(ml_full, joins & 1, kErrTreeSoftmax)) {
+                    ok = false;
+                    break;
+                }
+                ++joins;
+                const float2 a = ml[row], b = ml[kRows + row];
+                m = max_nan(a.x, b.x);
+                w0 = a.x == -INFINITY ? 0.f : ex2(a.x - m);
+                w1 = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+                l = fmaf(a.y, w0, b.y * w1);
+            }
+            tc_fence_after_sync();
+            if (act) {
+                const bool whole = walk.whole();
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const int c_lo = two ? 0 : t * (D / 64), c_hi = two ? D / 32 : c_lo + D / 64;
+                const int hd = row - tl * p.group;
+                uint16_t *orow = p.out + grow * p.out_token_stride +
+                                 static_cast<int64_t>(walk.head * p.group + hd) *
+                                     p.out_head_stride;
+                // The part's slot: the CTA's first part, or the one that begins a unit.
+                float *part = p.part + (static_cast<int64_t>(cta) * 4 + (walk.k0 == 0 ? 2 : 0) +
+                                        (two ? t : 0)) *
+                                           S::kPartFloats;
+                const bool odd = *odd_values != 0;
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; ++c) {
+                    uint32_t o[32];
+                    float x[32];
+                    if (two || other_steps) {
+                        const int g = two ? t : 1;
+                        tmem_ld_32x32b_x32(t_lanes + kOBase + g * D + c * 32, o);
+                        tmem_wait_ld_dep(o);
+                        const float w = two ? 1.f : w1;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = 0.f;
+                    }
+                    if (!two) {
+                        tmem_ld_32x32b_x32(t_lanes + kOBase + c * 32, o);
+                        tmem_wait_ld_dep(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = fmaf(__uint_as_float(o[e]), w0, x[e]);
+                    }
+                    if (odd && row < rows) {
+                        // Values that are not finite, of drafted tokens that this
+                        // row sees (their weights are positive).
+                        const int jlo = max(walk.k0 - r.ctx_tiles, 0) * kKeys;
+                        const int jhi = min((walk.k1 - r.ctx_tiles) * kKeys, r.n);
+#pragma unroll 1
+                        for (int jj = jlo; jj < jhi; ++jj) {
+                            const bool sees =
+                                mrow ? (jj >> 5) < p.words && ((mrow[jj >> 5] >> (jj & 31)) & 1)
+                                     : jj <= tok;
+                            if (!sees) continue;
+                            const uint16_t *vr =
+                                p.v + (static_cast<int64_t>(r.s0) + jj) * p.v_token_stride +
+                                walk.head * p.v_head_stride + c * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint16_t bits = vr[e];
+                                if constexpr (BF16) {
+                                    if ((bits & 0x7F80u) == 0x7F80u)
+                                        x[e] += __uint_as_float(static_cast<uint32_t>(bits) << 16);
+                                } else {
+                                    if ((bits & 0x7C00u) == 0x7C00u)
+                                        x[e] += __half2float(__ushort_as_half(bits));
+                                }
+                            }
+                        }
+                    }
+                    if (whole) {
+                        if (row < rows) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint4 u;
+                                u.x = pack2<BF16>(x[q * 8 + 0] * inv, x[q * 8 + 1] * inv);
+                                u.y = pack2<BF16>(x[q * 8 + 2] * inv, x[q * 8 + 3] * inv);
+                                u.z = pack2<BF16>(x[q * 8 + 4] * inv, x[q * 8 + 5] * inv);
+                                u.w = pack2<BF16>(x[q * 8 + 6] * inv, x[q * 8 + 7] * inv);
+                                *reinterpret_cast<uint4 *>(orow + c * 32 + q * 8) = u;
+                            }
+                        }
+                    } else if (row < rows) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) __stcg(part + (c * 32 + e) * kRows + row, x[e]);
+                    }
+                }
+                if (!whole && row < rows && (two || t == 0)) {
+                    __stcg(part + D * kRows + row, m);
+                    __stcg(part + (D + 1) * kRows + row, l);
+                }
+            }
+            // Outputs read: the next part's products may overwrite them.
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            ic += 2 * n;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem_base, kTmemCols);
+    }
+}
+
+// Joins the parts of the units that more than one CTA worked on:
+//   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s.
+// Block (c, y): the unit that began in CTA c's share, columns [8 y, 8 y + 8) of
+// both query tiles.  A block's threads are `rp` rows (a power of two that
+// covers the rows in use) times 512 / rp groups of parts, whose sums are added
+// up in order.  Bound by the latency of the partial results' loads (they lie
+// in L2); hence the many groups where there are few rows.
+constexpr int kJoinThreads = 512;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p)
+{
+    using S = TreeShape<D>;
+    __shared__ float s_acc[kJoinThreads][9];      // 8 columns and the sum
+    __shared__ float s_max[kJoinThreads];
+    const int c = blockIdx.x, col0 = blockIdx.y * 8, tid = threadIdx.x;
+    grid_dependency_wait();
+    const Split sp = p.split[c];
+    if (sp.ctas < 2) return;
+    const Request r = request(p, sp.b);
+    const int head = sp.unit / r.pairs, pair = sp.unit - head * r.pairs;
+    for (int t = 0; t < 2; ++t) {
+        const int tok0 = (2 * pair + t) * p.tile_tokens;
+        const int rows = min(p.tile_tokens, r.n - tok0) * p.group;
+        if (rows <= 0) break;
+        int rp = 8;
+        while (rp < rows) rp <<= 1;
+        const int groups = kJoinThreads / rp;
+        const int row = tid & (rp - 1), g = tid / rp;
+        const int per = (sp.ctas + groups - 1) / groups;
+        const int s0 = min(g * per, sp.ctas), s1 = min(s0 + per, sp.ctas);
+        // Part s lies in CTA c + s: the one that begins a unit, then first parts.
+        auto slot = [&](int s) {
+            return p.part +
+                   (static_cast<int64_t>(c + s) * 4 + (s == 0 ? 2 : 0) + t) * S::kPartFloats + row;
+        };
+        float mx = -INFINITY;
+        if (row < rows)
+            for (int s = s0; s < s1; ++s) mx = fmaxf(mx, __ldcg(slot(s) + D * kRows));
+        s_max[tid] = mx;
+        __syncthreads();
+        for (int i = 0; i < groups; ++i) mx = fmaxf(mx, s_max[i * rp + row]);
+        float acc[9];
+#pragma unroll
+        for (int e = 0; e < 9; ++e) acc[e] = 0.f;
+        if (row < rows)
+            for (int s = s0; s < s1; ++s) {
+                const float *part = slot(s);
+                const float ms = __ldcg(part + D * kRows);
+                const float w = ms == -INFINITY ? 0.f : ex2(ms - mx);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[e] = fmaf(__ldcg(part + (col0 + e) * kRows), w, acc[e]);
+                acc[8] = fmaf(__ldcg(part + (D + 1) * kRows), w, acc[8]);
+            }
+#pragma unroll
+        for (int e = 0; e < 9; ++e) s_acc[tid][e] = acc[e];
+        __syncthreads();
+        if (g == 0 && row < rows) {
+            for (int i = 1; i < groups; ++i)
+#pragma unroll
+                for (int e = 0; e < 9; ++e) acc[e] += s_acc[i * rp + row][e];
+            const float inv = acc[8] > 0.f ? 1.f / acc[8] : 0.f;
+            const int tl = row / p.group, hd = row - tl * p.group;
+            uint4 u;
+            u.x = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+            u.y = pack2<BF16>(acc[2] * inv, acc[3] * inv);
+            u.z = pack2<BF16>(acc[4] * inv, acc[5] * inv);
+            u.w = pack2<BF16>(acc[6] * inv, acc[7] * inv);
+            *reinterpret_cast<uint4 *>(
+                p.out + (static_cast<int64_t>(r.s0) + tok0 + tl) * p.out_token_stride +
+                static_cast<int64_t>(head * p.group + hd) * p.out_head_stride + col0) = u;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace tgt
+
+namespace {
+
+using namespace tgc;
+
+constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
+
+// A tensor map of 16-bit elements: dims from the head dimension outwards with
+// the strides (in elements) of all but the first; a box of 64 elements by
+// `rows` along the dimensions that have a box extent.
+bool encode_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *tm, const void *base,
+                bool bf16, int rank, const int64_t *dims, const int64_t *strides,
+                const uint32_t *box)
+{
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        bx[i] = box[i];
+    }
+    // The stride of a dimension of extent 1 is never used; it only has to be valid.
+    for (int i = 0; i + 1 < rank; ++i)
+        st[i] = dims[i + 1] > 1 ? static_cast<cuuint64_t>(strides[i]) * 2 : 128;
+    return encode(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  rank, const_cast<void *>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+    CUtensorMap q, kc, vc, k, v;
+};
+
+template <int D, bool BF16>
+tg_status_t launch(const Maps &maps, const tgt::TreeParams &p, int grid, cudaStream_t stream)
+{
+    using S = tgt::TreeShape<D>;
+    // One bit per device: the kernel's dynamic shared-memory limit is raised.
+    static std::atomic<uint64_t> attr_set{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return TG_ERR_UNSUPPORTED_DEVICE;
+    }
+    const uint64_t bit = uint64_t(1) << dev;
+    if (!(attr_set.load() & bit)) {
+        if (cudaFuncSetAttribute(tgt::tree_attn_kernel<D, BF16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kDynamicBytes) != cudaSuccess) {
+            cudaGetLastError();
+            return TG_ERR_LAUNCH;
+        }
+        attr_set.fetch_or(bit);
+    }
+    tgt::tree_attn_kernel<D, BF16><<<grid, tgt::kThreads, S::kDynamicBytes, stream>>>(
+        maps.q, maps.kc, maps.vc, maps.k, maps.v, p);
+    if (cudaGetLastError() != cudaSuccess) return TG_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, D / 8);
+    cfg.blockDim = dim3(tgt::kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, tgt::tree_join_kernel<D, BF16>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    return TG_OK;
+}
+
+constexpr int64_t kMaxStride = int64_t(1) << 38;    // elements; a map's strides are below 2^40 bytes
+
+tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t stream)
+{
+    const int shift = page_shift_of(a.page_size);
+    if ((a.type != TG_TYPE_FP16 && a.type != TG_TYPE_BF16) || a.tokens < 0 || a.tokens >= kInt32 ||
+        a.batch < 0 || a.batch >= kInt32 - 1024 || a.kv_heads < 0 || a.kv_heads > (1 << 20) ||
+        a.group < 1 || a.group > 128 || (a.head_dim != 64 && a.head_dim != 128) || shift < 0 ||
+        a.num_pages < 0 || a.num_pages >= kInt32 || a.max_pages < 0 ||
+        a.max_pages >= (kInt32 - 256) >> shift || a.table_stride < a.max_pages ||
+        a.table_stride >= kInt32 || !std::isfinite(a.scale) || a.scale < 0.f ||
+        (a.scale != 0.f && a.scale < 1e-30f) ||
+        (a.inject != 0 && a.inject != TG_INJECT_SKIP_FIRST_LOAD))
+        return TG_ERR_INVALID_ARG;
+    if (a.mask && (a.words < 1 || a.words > (1 << 26) || a.mask_stride < a.words ||
+                   a.mask_stride >= kInt32))
+        return TG_ERR_INVALID_ARG;
+    // Query tiles of all key heads, and 32-bit key indexes.
+    const int64_t tile_tokens = tgt::kRows / a.group;
+    if (a.kv_heads * (a.tokens / tile_tokens + 2) >= kInt32 || a.tokens >= kInt32 - 256)
+        return TG_ERR_INVALID_ARG;
+    if (a.tokens == 0 || a.batch == 0 || a.kv_heads == 0) return TG_OK;
+    if (!a.q || !a.k || !a.v || !a.out || !a.lens || !a.starts || !a.workspace ||
+        a.workspace_bytes < tg_tree_attention_workspace_size(a.head_dim))
+        return TG_ERR_INVALID_ARG;
+    const bool cache = a.num_pages > 0 && a.max_pages > 0;
+    if (cache && (!a.k_cache || !a.v_cache || !a.block_tables)) return TG_ERR_INVALID_ARG;
+
+    const int64_t heads = a.kv_heads * a.group, D = a.head_dim;
+    // Strides of dimensions with more than one element.
+    const Dim strides[] = {{a.tokens, a.q_token_stride},
+                             {heads, a.q_head_stride},
+                             {a.tokens, a.kv_token_stride},
+                             {a.kv_heads, a.kv_head_stride},
+                             {a.tokens, a.out_token_stride},
+                             {heads, a.out_head_stride},
+                             {cache ? a.num_pages : 1, a.page_stride},
+                             {cache ? a.page_size : 1, a.slot_stride},
+                             {cache ? a.kv_heads : 1, a.cache_head_stride}};
+    for (const Dim &c : strides)
+        if (c.n > 1 && (c.stride < D || c.stride >= kMaxStride)) return TG_ERR_INVALID_ARG;
+    for (const Dim &c : strides)
+        if (c.n > 1 && (c.stride & 7)) return TG_ERR_MISALIGNED;
+    const void *vec[] = {a.q, a.k, a.v, a.out};
+    for (const void *q : vec)
+        if (misaligned(q, 16)) return TG_ERR_MISALIGNED;
+    if (cache && (misaligned(a.k_cache, 16) || misaligned(a.v_cache, 16))) return TG_ERR_MISALIGNED;
+    if (misaligned(a.workspace, 256) || misaligned(a.lens, 4) || misaligned(a.starts, 4) ||
+        misaligned(a.block_tables, 4) || misaligned(a.mask, 4))
+        return TG_ERR_MISALIGNED;
+
+    const size_t new_bytes =
+        extent({{a.tokens, a.kv_token_stride}, {a.kv_heads, a.kv_head_stride}}, D);
+    const size_t cache_bytes = cache ? extent({{a.num_pages, a.page_stride},
+                                               {a.page_size, a.slot_stride},
+                                               {a.kv_heads, a.cache_head_stride}},
+                                              D)
+                                     : 0;
+    const Range in[] = {
+        {a.q, extent({{a.tokens, a.q_token_stride}, {heads, a.q_head_stride}}, D)},
+        {a.k, new_bytes},
+        {a.v, new_bytes},
+        {a.k_cache, cache_bytes},
+        {a.v_cache, cache_bytes},
+        {a.block_tables,
+         cache ? static_cast<size_t>((a.batch - 1) * a.table_stride + a.max_pages) * 4 : 0},
+        {a.lens, static_cast<size_t>(a.batch) * 4},
+        {a.starts, static_cast<size_t>(a.batch + 1) * 4},
+        {a.mask, a.mask ? static_cast<size_t>((a.tokens - 1) * a.mask_stride + a.words) * 4 : 0}};
+    const Range out = {a.out,
+                       extent({{a.tokens, a.out_token_stride}, {heads, a.out_head_stride}}, D)};
+    const Range ws = {a.workspace, tg_tree_attention_workspace_size(a.head_dim)};
+    for (const Range &i : in)
+        if (overlap(out, i) || overlap(ws, i)) return TG_ERR_INVALID_ARG;
+    if (overlap(out, ws)) return TG_ERR_INVALID_ARG;
+
+    int num_sms = 0;
+    unsigned *error_word = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const tg_status_t st = tg_internal_device(&num_sms, &error_word, &encode);
+    if (st != TG_OK) return st;
+
+    const bool bf16 = a.type == TG_TYPE_BF16;
+    Maps maps;
+    {
+        const int64_t dims[] = {D, heads, a.tokens};
+        const int64_t str[] = {a.q_head_stride, a.q_token_stride};
+        const uint32_t box[] = {tgt::kAtom, static_cast<uint32_t>(a.group),
+                                static_cast<uint32_t>(tile_tokens)};
+        if (!encode_map(encode, &maps.q, a.q, bf16, 3, dims, str, box)) return TG_ERR_CUDA;
+    }
+    {
+        const int64_t dims[] = {D, a.tokens, a.kv_heads};
+        const int64_t str[] = {a.kv_token_stride, a.kv_head_stride};
+        const uint32_t box[] = {tgt::kAtom, tgt::kKeys, 1};
+        if (!encode_map(encode, &maps.k, a.k, bf16, 3, dims, str, box) ||
+            !encode_map(encode, &maps.v, a.v, bf16, 3, dims, str, box))
+            return TG_ERR_CUDA;
+    }
+    if (cache) {
+        const int64_t dims[] = {D, a.page_size, a.kv_heads, a.num_pages};
+        const int64_t str[] = {a.slot_stride, a.cache_head_stride, a.page_stride};
+        const uint32_t box[] = {
+            tgt::kAtom, static_cast<uint32_t>(a.page_size < tgt::kKeys ? a.page_size : tgt::kKeys),
+            1, 1};
+        if (!encode_map(encode, &maps.kc, a.k_cache, bf16, 4, dims, str, box) ||
+            !encode_map(encode, &maps.vc, a.v_cache, bf16, 4, dims, str, box))
+            return TG_ERR_CUDA;
+    } else {
+        maps.kc = maps.k;     // not read: every context is empty
+        maps.vc = maps.v;
+    }
+
+    tgt::TreeParams p;
+    p.lens = a.lens;
+    p.starts = a.starts;
+    p.tables = a.block_tables;
+    p.mask = a.mask;
+    p.v = static_cast<const uint16_t *>(a.v);
+    p.out = static_cast<uint16_t *>(a.out);
+    p.v_token_stride = a.kv_token_stride;
+    p.v_head_stride = a.kv_head_stride;
+    p.out_token_stride = a.out_token_stride;
+    p.out_head_stride = a.out_head_stride;
+    p.table_stride = a.table_stride;
+    p.max_len = cache ? a.max_pages << shift : 0;
+    p.mask_stride = a.mask_stride;
+    p.tokens = static_cast<int>(a.tokens);
+    p.batch = static_cast<int>(a.batch);
+    p.kv_heads = static_cast<int>(a.kv_heads);
+    p.group = static_cast<int>(a.group);
+    p.tile_tokens = static_cast<int>(tile_tokens);
+    p.words = static_cast<int>(a.words);
+    p.page_shift = shift;
+    const float scale = a.scale != 0.f ? a.scale : 1.0f / std::sqrt(static_cast<float>(D));
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.split = static_cast<tgt::Split *>(a.workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tgt::split_bytes());
+    p.inject = a.inject;
+    p.wait_limit_ns = a.wait_limit_ns ? a.wait_limit_ns : kDefaultWaitLimitNs;
+    p.error_word = error_word;
+    const int grid = num_sms < tgt::kMaxCtas ? num_sms : tgt::kMaxCtas;
+    if (D == 64)
+        return bf16 ? launch<64, true>(maps, p, grid, stream)
+                    : launch<64, false>(maps, p, grid, stream);
+    return bf16 ? launch<128, true>(maps, p, grid, stream)
+                : launch<128, false>(maps, p, grid, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tg_tree_attention_workspace_size(int64_t head_dim)
+{
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return tgt::split_bytes() + sizeof(float) * static_cast<size_t>(tgt::kMaxCtas) * 4 *
+                                    static_cast<size_t>((head_dim + 2) * tgt::kRows);
+}
+
+tg_status_t tg_tree_attention(const tg_tree_attention_t *args, void *stream)
+{
+    if (!args) return TG_ERR_INVALID_ARG;
+    return tree_attention_impl(*args, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
