@@ -28,10 +28,14 @@
 //   warp 8          TMA producer: queries, and keys and values through one
 //                   ring in the order in which the products need them.
 //   warp 9          TMEM allocator and MMA issuer.
-// Step i belongs to group t = i mod 2.  The issuer's order is S_0 S_1, then
-// P_i V, S_i+2 for i = 0, 1, ...; P_i (16 bits) overwrites S_i in tensor
-// memory, and S_i+2 follows P_i V in the tensor pipe's order.
-// TMEM: S_t / P_t at columns 128 t, O_t at 256 + D t.
+// Step i (a key tile of a query tile) belongs to group t = i mod 2 and has two
+// halves of 64 keys, each with its own score columns.  The issuer's order is
+// S_0 S_1, then for i = 0, 1, ... and each half h: P_i,h V, S_i+2,h.  P_i,h (16
+// bits) overwrites S_i,h in tensor memory, and S_i+2,h follows P_i,h V in the
+// tensor pipe's order; while a group exponentiates one half, the other half's
+// product and next scores are made, so it does not wait for them.  A half that
+// lies past the last key is left out by all.
+// TMEM: S_t,h / P_t,h at columns 128 t + 64 h, O_t at 256 + D t.
 //
 // Masked places.  A masked score becomes -inf before the maximum.  A masked
 // key's value still enters the product with weight 0, so values that are not
@@ -61,7 +65,8 @@ namespace tgt {
 using namespace tga;
 
 constexpr int kRows = 128;         // query rows of a tile (TMEM lanes)
-constexpr int kKeys = 128;         // keys of a tile (score columns)
+constexpr int kKeys = 128;         // keys of a tile
+constexpr int kHalf = 64;          // keys of a half step (score columns)
 constexpr int kAtom = 64;          // head-dim elements per 128-byte swizzle atom
 constexpr int kAtomBytes = 128 * 128;
 constexpr int kProducerWarp = 8;
@@ -80,9 +85,10 @@ constexpr unsigned kErrTreeDrain = 8192u;
 constexpr unsigned kErrTreeSmem = 16384u;
 
 // What a CTA leaves for the joining kernel: the unit that begins in its share
-// and goes on behind it, and how many CTAs have a part of it (0: none).
+// and goes on behind it (first row of the packing, its key head, rows of its
+// two query tiles), and how many CTAs have a part of it (0: none).
 struct Split {
-    int b, unit, ctas, pad;
+    int ctas, head, first, rows[2], pad[3];
 };
 
 struct TreeParams {
@@ -111,9 +117,9 @@ struct TreeShape {
     static constexpr int kKVOff = 2 * kTileBytes;
     static constexpr int kMlOff = kKVOff + kStages * kTileBytes;   // (m, l) of both groups
     static constexpr int kBarOff = kMlOff + 2 * kRows * 8;
-    // q_full[2], q_empty[2], kv_full[], kv_empty[], s_full[2], p_full[2], o_full[2],
-    // o_free, ml_full, drain
-    static constexpr int kNumBars = 4 + 2 * kStages + 6 + 3;
+    // q_full[2], q_empty[2], kv_full[], kv_empty[], s_full[2][2], p_full[2][2],
+    // pv_done[2][2], o_free, ml_full, drain
+    static constexpr int kNumBars = 4 + 2 * kStages + 12 + 3;
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
     static constexpr int kFlagOff = kAbortOff + 4;
@@ -139,6 +145,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 // Instruction descriptor bits that select bf16 for A and B.
 template <bool BF16>
 constexpr uint32_t kTypeBits = BF16 ? (1u << 7) | (1u << 10) : 0u;
+
+// True in one lane of the (converged) warp, the same one every time.  A branch
+// on it tells the compiler that one thread runs it, so that the descriptors of
+// the products are kept in uniform registers; behind `lane == 0` each product
+// took about 110 cycles to issue, more than the tensor core needs for it.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// The largest of three, NaN if one is (one instruction on sm_100).
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const CUtensorMap *tm,
                                             uint64_t *bar, int32_t x, int32_t y, int32_t z,
@@ -178,47 +205,59 @@ __device__ __forceinline__ Request request(const TreeParams &p, int b)
 }
 
 // The parts of units in a CTA's share, in order; every warp walks through them
-// by itself, all lanes together.
+// by itself, all lanes together.  Where a share begins is found once per CTA.
 struct Walk {
-    int64_t pos, end;    // what is left of the share, in key tiles
-    int64_t base;        // where request b's work begins
+    int64_t left;        // key tiles left of the share, from the current part's end
     int b;
     Request r;
     // the current part: key tiles [k0, k1) of a unit
-    int unit, head, pair, k0, k1;
+    int head, pair, k0, k1;
     bool two;            // both query tiles of the pair exist
 
+    __device__ __forceinline__ void part()
+    {
+        k1 = left < r.nk - k0 ? k0 + static_cast<int>(left) : r.nk;
+        left -= k1 - k0;
+        two = 2 * pair + 1 < r.q_tiles;
+    }
+    // The next part (k0 == k1 < nk: the first one, set up by the caller).
     __device__ __forceinline__ bool next(const TreeParams &p, int lane)
     {
-        if (pos >= end) return false;
-        if (pos >= base + r.work) {
-            base += r.work;
-            // the next request that has work
-            for (;;) {
-                const int mine = b + 1 + lane;
-                const bool has = mine < p.batch && request(p, mine).work > 0;
-                const unsigned any = __ballot_sync(0xffffffffu, has);
-                if (any) {
-                    b += __ffs(any);
-                    break;
-                }
-                b += 32;
-                if (b >= p.batch) return false;
+        if (left <= 0) return false;
+        if (k1 == r.nk) {
+            k0 = 0;
+            if (++pair == r.pairs) {
+                pair = 0;
+                ++head;
             }
-            r = request(p, b);
+            if (head == p.kv_heads) {
+                head = 0;
+                // the next request that has work
+                for (;;) {
+                    const int mine = b + 1 + lane;
+                    const bool has = mine < p.batch && request(p, mine).work > 0;
+                    const unsigned any = __ballot_sync(0xffffffffu, has);
+                    if (any) {
+                        b += __ffs(any);
+                        break;
+                    }
+                    b += 32;
+                    if (b >= p.batch) return false;
+                }
+                r = request(p, b);
+            }
         }
-        const int64_t rel = pos - base;
-        unit = static_cast<int>(rel / r.nk);
-        k0 = static_cast<int>(rel - static_cast<int64_t>(unit) * r.nk);
-        const int64_t left = end - pos;
-        k1 = left < r.nk - k0 ? k0 + static_cast<int>(left) : r.nk;
-        pos += k1 - k0;
-        head = unit / r.pairs;
-        pair = unit - head * r.pairs;
-        two = 2 * pair + 1 < r.q_tiles;
+        part();
         return true;
     }
     __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == r.nk; }
+    // Keys of key tile kj from its first on (more than 128 where it is full),
+    // and its halves that have any.
+    __device__ __forceinline__ int keys(int kj) const
+    {
+        return kj >= r.ctx_tiles ? r.n - (kj - r.ctx_tiles) * kKeys : r.ctx - kj * kKeys;
+    }
+    __device__ __forceinline__ int halves(int kj) const { return keys(kj) > kHalf ? 2 : 1; }
 };
 
 template <int D, bool BF16>
@@ -239,10 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *q_empty = bars + 2;
     uint64_t *kv_full = bars + 4;
     uint64_t *kv_empty = kv_full + NS;
-    uint64_t *s_full = kv_empty + NS;    // [2]: S_t is in TMEM
-    uint64_t *p_full = s_full + 2;       // [2]: P_t is in TMEM (4 arrivals)
-    uint64_t *o_full = p_full + 2;       // [2]: O_t of the part complete
-    uint64_t *o_free = o_full + 2;       // both O read (8 arrivals)
+    uint64_t *s_full = kv_empty + NS;    // [2 t + h]: S_t,h is in TMEM
+    uint64_t *p_full = s_full + 4;       // [2 t + h]: P_t,h is in TMEM (4 arrivals)
+    uint64_t *pv_done = p_full + 4;      // [2 t + k mod 2]: group t's product number k is complete
+    uint64_t *o_free = pv_done + 4;      // both O read (8 arrivals)
     uint64_t *ml_full = o_free + 1;      // both groups' m and l written (8 arrivals)
     uint64_t *drain_bar = ml_full + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kTmemSlotOff);
@@ -260,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // above); uniform over the CTA.
     if (sbase & 1023u) {
         if (threadIdx.x == 0) {
-            p.split[cta] = Split{0, 0, 0, 0};
+            p.split[cta].ctas = 0;
             atomicOr(p.error_word, kErrTreeSmem);
         }
         return;
@@ -269,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kNumBars; ++i) {
             uint64_t *bar = &bars[i];
-            const uint32_t count = (bar == &p_full[0] || bar == &p_full[1]) ? 4u
-                                   : (bar == o_free || bar == ml_full)      ? 8u
-                                                                            : 1u;
+            const uint32_t count = (bar >= p_full && bar < pv_done)    ? 4u
+                                   : (bar == o_free || bar == ml_full) ? 8u
+                                                                       : 1u;
             mbar_init(bar, count);
         }
         *abort_flag = 0;
@@ -290,74 +329,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish<1>();
     }
 
-    // Share of this CTA.  Scratch in the ring, which is not in use yet.
-    int64_t *scr = reinterpret_cast<int64_t *>(smem + S::kKVOff);
-    int64_t *scr_sum = scr, *scr_scan = scr + kWarps, *scr_base = scr + 2 * kWarps;
-    int *scr_b = reinterpret_cast<int *>(scr_base + 1);
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) mine += request(p, b).work;
+    // Share of this CTA: sums of the requests' work over the threads, each of
+    // which has a run of them.  Scratch in the ring, which is not in use yet.
+    struct Scratch {
+        int64_t sum[kWarps];
+        Walk walk;
+    };
+    Scratch &scr = *reinterpret_cast<Scratch *>(smem + S::kKVOff);
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
+    int64_t work = 0;
+    for (int b = b0; b < b1; ++b) work += request(p, b).work;
+    int64_t incl = work;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    if (lane == 0) scr_sum[warp] = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) scr.sum[warp] = incl;
     __syncthreads();
-    int64_t total = 0;
+    int64_t hi = incl, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += scr_sum[w];
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) hi += scr.sum[w];
+        total += scr.sum[w];
+    }
     const int64_t share = (total + gridDim.x - 1) / gridDim.x;
     const int64_t pos0 = min(total, cta * share);
     const int64_t pos1 = min(total, pos0 + share);
-    if (pos0 == pos1 && threadIdx.x == 0) p.split[cta] = Split{0, 0, 0, 0};
-    int64_t before = 0;      // work of the requests before this chunk
-    for (int c0 = 0; c0 < p.batch && before < pos1 && pos0 < pos1; c0 += kThreads) {
-        const int b = c0 + threadIdx.x;
-        const Request r = b < p.batch ? request(p, b) : Request{0, 0, 0, 0, 0, 0, 0, 0};
-        int64_t incl = r.work;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
+    if (pos0 == pos1 && threadIdx.x == 0) p.split[cta].ctas = 0;
+    // The threads whose runs hold the share's first and last key tile.
+    int64_t lo = hi - work;
+    if (pos0 < pos1 && lo < pos1 && hi > pos0) {
+        for (int b = b0; b < b1 && lo < pos1; ++b) {
+            const Request r = request(p, b);
+            const int64_t end = lo + r.work;
+            if (lo <= pos0 && pos0 < end) {
+                Walk w;
+                const int64_t rel = pos0 - lo;
+                const int unit = static_cast<int>(rel / r.nk);
+                w.left = pos1 - pos0;
+                w.b = b;
+                w.r = r;
+                w.head = unit / r.pairs;
+                w.pair = unit - w.head * r.pairs;
+                w.k0 = w.k1 = static_cast<int>(rel - static_cast<int64_t>(unit) * r.nk);
+                w.two = false;
+                scr.walk = w;
+            }
+            if (lo < pos1 && pos1 <= end) {
+                // The unit that holds the share's last key tile.
+                const int64_t u = (pos1 - 1 - lo) / r.nk;
+                const int64_t ubegin = lo + u * r.nk, uend = ubegin + r.nk;
+                Split sp = {};
+                if (ubegin >= pos0 && uend > pos1)
+                    sp.ctas = static_cast<int>((uend - 1) / share) - cta + 1;
+                sp.head = static_cast<int>(u) / r.pairs;
+                const int tok0 = 2 * (static_cast<int>(u) - sp.head * r.pairs) * p.tile_tokens;
+                sp.first = r.s0 + tok0;
+                for (int t = 0; t < 2; ++t)
+                    sp.rows[t] =
+                        max(0, min(p.tile_tokens, r.n - tok0 - t * p.tile_tokens)) * p.group;
+                p.split[cta] = sp;
+            }
+            lo = end;
         }
-        if (lane == 31) scr_scan[warp] = incl;
-        __syncthreads();
-        int64_t off = before, sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) off += scr_scan[w];
-            sum += scr_scan[w];
-        }
-        const int64_t lo = off + incl - r.work, hi = off + incl;
-        if (lo <= pos0 && pos0 < hi) {
-            *scr_base = lo;
-            *scr_b = b;
-        }
-        if (lo < pos1 && pos1 <= hi) {
-            // The unit that holds the share's last key tile.
-            const int64_t u = (pos1 - 1 - lo) / r.nk;
-            const int64_t ubegin = lo + u * r.nk, uend = ubegin + r.nk;
-            const bool split = ubegin >= pos0 && uend > pos1;
-            const int ctas = split ? static_cast<int>((uend - 1) / share) - cta + 1 : 0;
-            p.split[cta] = Split{b, static_cast<int>(u), ctas, 0};
-        }
-        before += sum;
-        __syncthreads();     // scr_scan is written again
     }
-    __syncthreads();
-    Walk walk;
-    walk.pos = pos0;
-    walk.end = pos1;
-    walk.base = 0;
-    walk.b = 0;
-    if (pos0 < pos1) {
-        walk.base = *scr_base;
-        walk.b = *scr_b;
-        walk.r = request(p, walk.b);
-    }
-    // The scratch is read before the ring's first copies land on it.
-    fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    Walk walk;
+    walk.left = 0;
+    if (pos0 < pos1) walk = scr.walk;
+    // The scratch is read before the ring's first copies land on it.
+    fence_proxy_async_smem();
+    __syncthreads();
 
     auto wait_all = [&](uint64_t *bar, uint32_t parity, unsigned site) -> bool {
         const bool ok = mbar_wait_bounded(bar, parity, abort_flag, limit, p.error_word, site);
@@ -456,75 +503,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        constexpr uint32_t kIdescS = idesc_f16_f32_kk(kRows, kKeys) | kTypeBits<BF16>;
+        constexpr uint32_t kIdescS = idesc_f16_f32_kk(kRows, kHalf) | kTypeBits<BF16>;
         constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | kTypeBits<BF16>;
+        constexpr uint32_t kHalfBytes = kHalf * 128;      // 64 rows of a 128-byte atom
         uint32_t qc = 0, ic = 0, parts = 0;
-        uint32_t steps[2] = {0, 0};     // products P V issued, per group
+        uint32_t p_phase = 0;           // bit 2 t + h: parity of the next P_t,h
+        uint32_t pv_next = 0;           // bit t: parity of group t's next product's number
         bool ok = true, issued = false;
         while (ok && walk.next(p, lane)) {
             const bool two = walk.two;
             const int n = walk.k1 - walk.k0;
             const int N = two ? 2 * n : n;
-            auto stage_k = [&](int j) { return j == 0 ? ic : ic + 2 * j - 1; };
-            auto stage_v = [&](int j) { return j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2; };
-            // S_i = Q K^T
-            auto issue_s = [&](int i) -> bool {
-                const int t = i & 1, j = two ? i >> 1 : i;
-                const uint32_t qi = two ? qc + t : qc, qs = qi & 1u;
-                const uint32_t item = stage_k(j), st = item % NS;
-                if (!wait_all(&q_full[qs], (qi >> 1) & 1, kErrTreeMma)) return false;
-                if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeMma)) return false;
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t qa = sbase + S::kQOff + qs * S::kTileBytes;
-                    const uint32_t ka = sbase + S::kKVOff + st * S::kTileBytes;
+            // One thread waits and issues for the whole part.  The tensor core
+            // takes few products ahead, so what lies between two of them is kept
+            // short: nothing is waited for twice.
+            if (elect_lane()) {
+                auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+                    return mbar_wait_bounded(bar, parity, abort_flag, limit, p.error_word,
+                                             kErrTreeMma);
+                };
+                // S_i,h = Q K_h^T
+                auto issue_s = [&](int i, int h, int halves) -> bool {
+                    const int t = i & 1, j = two ? i >> 1 : i;
+                    const uint32_t qi = two ? qc + t : qc, qs = qi & 1u;
+                    const uint32_t item = j == 0 ? ic : ic + 2 * j - 1, st = item % NS;
+                    if (h == 0) {
+                        if (i < 2 && (two || i == 0) && !wait(&q_full[qs], (qi >> 1) & 1))
+                            return false;
+                        if ((!two || t == 0) && !wait(&kv_full[st], (item / NS) & 1)) return false;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t qd =
+                        smem_desc_sw128(sbase + S::kQOff + qs * S::kTileBytes, 16, 1024);
+                    const uint64_t kd = smem_desc_sw128(
+                        sbase + S::kKVOff + st * S::kTileBytes + h * kHalfBytes, 16, 1024);
+                    const uint32_t ds = tmem_base + t * kKeys + h * kHalf;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kAtomBytes + (kk & 3) * 32;
-                        mma_f16_ss<1>(tmem_base + t * kKeys, smem_desc_sw128(qa + off, 16, 1024),
-                                      smem_desc_sw128(ka + off, 16, 1024), kIdescS, kk > 0);
+                        // a descriptor counts in 16 bytes
+                        const uint64_t off = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) / 16;
+                        mma_f16_ss<1>(ds, qd + off, kd + off, kIdescS, kk > 0);
                     }
-                    mma_commit<1>(&s_full[t]);
-                    if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
-                    if (two ? i + 2 >= N : i + 1 == N) mma_commit<1>(&q_empty[qs]);
-                }
-                __syncwarp();
-                issued = true;
-                return true;
-            };
-            // O_t += P_i V
-            auto issue_pv = [&](int i) -> bool {
-                const int t = i & 1, j = two ? i >> 1 : i;
-                const uint32_t item = stage_v(j), st = item % NS;
-                if (i < 2 && parts > 0 && !wait_all(o_free, (parts - 1) & 1, kErrTreeMma))
-                    return false;
-                if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeMma)) return false;
-                if (!wait_all(&p_full[t], steps[t] & 1, kErrTreeMma)) return false;
-                ++steps[t];
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t va = sbase + S::kKVOff + st * S::kTileBytes;
+                    mma_commit<1>(&s_full[2 * t + h]);
+                    if (h + 1 == halves) {
+                        if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
+                        if (two ? i + 2 >= N : i + 1 == N) mma_commit<1>(&q_empty[qs]);
+                    }
+                    return true;
+                };
+                // O_t += P_i,h V_h
+                auto issue_pv = [&](int i, int h, int halves) -> bool {
+                    const int t = i & 1, j = two ? i >> 1 : i;
+                    const uint32_t item = j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2;
+                    const uint32_t st = item % NS;
+                    if (h == 0) {
+                        if (i == 0 && parts > 0 && !wait(o_free, (parts - 1) & 1)) return false;
+                        if ((!two || t == 0) && !wait(&kv_full[st], (item / NS) & 1)) return false;
+                    }
+                    const uint32_t pb = 2 * t + h;
+                    if (!wait(&p_full[pb], (p_phase >> pb) & 1)) return false;
+                    p_phase ^= 1u << pb;
+                    tc_fence_after_sync();
+                    const uint64_t vd =
+                        smem_desc_sw128(sbase + S::kKVOff + st * S::kTileBytes + h * kHalfBytes,
+                                        kAtomBytes, 1024);
+                    const uint32_t od = tmem_base + kOBase + t * D;
+                    const uint32_t pa = tmem_base + t * kKeys + h * kHalf;
+                    const uint32_t more = i >= 2 || h > 0;
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(tmem_base + kOBase + t * D, tmem_base + t * kKeys + kk * 8,
-                                   smem_desc_sw128(va + kk * 2048, kAtomBytes, 1024), kIdescO,
-                                   (i >= 2 || kk > 0) ? 1u : 0u);
-                    if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
-                    if (i + 2 >= N) mma_commit<1>(&o_full[t]);
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        mma_f16_ts(od, pa + kk * 8, vd + kk * (2048 / 16), kIdescO,
+                                   kk > 0 ? 1u : more);
+                    mma_commit<1>(&pv_done[2 * t + ((pv_next >> t) & 1)]);
+                    pv_next ^= 1u << t;
+                    if (h + 1 == halves && (!two || t == 1)) mma_commit<1>(&kv_empty[st]);
+                    return true;
+                };
+                auto halves_of = [&](int i) { return walk.halves(walk.k0 + (two ? i >> 1 : i)); };
+                bool good = true;
+                for (int i = 0; good && i < 2 && i < N; ++i) {
+                    const int hn = halves_of(i);
+                    for (int h = 0; good && h < hn; ++h) good = issue_s(i, h, hn);
                 }
-                __syncwarp();
-                return true;
-            };
-            ok = issue_s(0) && (N < 2 || issue_s(1));
-            for (int i = 0; ok && i < N; ++i) {
-                ok = issue_pv(i);
-                if (ok && i + 2 < N) ok = issue_s(i + 2);
+                for (int i = 0; good && i < N; ++i) {
+                    const int hn = halves_of(i), hs = i + 2 < N ? halves_of(i + 2) : 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (good && h < hn) good = issue_pv(i, h, hn);
+                        if (good && h < hs) good = issue_s(i + 2, h, hs);
+                    }
+                }
+                ok = good;
             }
+            ok = __all_sync(0xffffffffu, ok);
+            issued = true;
             qc += two ? 2 : 1;
             ic += 2 * n;
             ++parts;
         }
-        if (issued && lane == 0) {
+        if (issued && elect_lane()) {
             mma_commit<1>(drain_bar);
             if (!mbar_wait_drain(drain_bar, 0, limit)) atomicOr(p.error_word, kErrTreeDrain);
         }
@@ -535,140 +612,154 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t t_s = t_lanes + t * kKeys;
         const float sl2 = p.scale_log2;
-        uint32_t ic = 0, steps = 0, joins = 0;
-        uint32_t outs[2] = {0, 0};      // parts in which group 0, group 1 had steps
+        const int tl = row / p.group, hd = row - tl * p.group;
+        uint32_t ic = 0, joins = 0;
+        uint32_t s_phase = 0;           // bit h: parity of the next S_t,h
+        uint32_t pv = 0;                // products P V of this group in the parts before
+        uint32_t parts = 0;
         bool ok = true;
+        // Waits for this group's product number k.  Scores k came after product
+        // k - 2, so the barrier that k shares with k - 2 is in k's phase or past it.
+        auto wait_pv = [&](uint32_t k) -> bool {
+            ok = wait_all(&pv_done[2 * t + (k & 1)], (k >> 1) & 1, kErrTreeSoftmax);
+            return ok;
+        };
         while (ok && walk.next(p, lane)) {
             const Request &r = walk.r;
             const bool two = walk.two;
             const int n = walk.k1 - walk.k0;
             const int N = two ? 2 * n : n;
-            const int tile = 2 * walk.pair + (two ? t : 0);
-            const int tok0 = tile * p.tile_tokens;
+            const int tok0 = (2 * walk.pair + (two ? t : 0)) * p.tile_tokens;
             const int rows = min(p.tile_tokens, r.n - tok0) * p.group;
             const bool act = quarter * 32 < rows;        // uniform over the warp
-            const int tl = row / p.group;
             const int tok = tok0 + tl;                   // of the request
             const int64_t grow = static_cast<int64_t>(r.s0) + tok;
             const int32_t *mrow = p.mask ? p.mask + grow * p.mask_stride : nullptr;
-            float m = -INFINITY;   // running maximum of the scaled scores, log2 units
-            float l = 0.f;         // running sum of 2^(score - m)
+            uint32_t done = pv;     // products of this group before the next
+            float m = -INFINITY;    // running maximum of the scaled scores, log2 units
+            float l = 0.f;          // running sum of 2^(score - m)
             for (int i = t; ok && i < N; i += 2) {
                 const int j = two ? i >> 1 : i;
                 const int kj = walk.k0 + j;
                 const bool tree = kj >= r.ctx_tiles;
-                const int key0 = (kj - r.ctx_tiles) * kKeys;       // first drafted key (tree)
-                const int lim = tree ? r.n - key0 : r.ctx - kj * kKeys;
+                const int lim = walk.keys(kj);
                 const bool edge = tree || lim < kKeys;             // not wholly visible
-                if (!wait_all(&s_full[t], steps & 1, kErrTreeSoftmax)) {
-                    ok = false;
-                    break;
-                }
-                ++steps;
-                tc_fence_after_sync();
-                if (act) {
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_s + q * 32, s[q]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_wait_ld_dep(s[q]);
-                    if (edge) {
-                        // Visible columns: keys that exist, and for drafted ones
-                        // the row's mask (or, without one, keys up to its own).
-                        const int lim_row = tree && !mrow ? min(lim, tok + 1 - key0) : lim;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int v = lim_row - 32 * q;
-                            uint32_t vis = v >= 32 ? 0xffffffffu : (v <= 0 ? 0u : (1u << v) - 1u);
-                            if (tree && mrow) {
-                                const int w = (key0 >> 5) + q;
-                                vis &= row < rows && w < p.words
-                                           ? static_cast<uint32_t>(mrow[w])
-                                           : 0u;
-                            }
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!((vis >> c) & 1u)) s[q][c] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                    // The maximum keeps NaN (a NaN score makes the row NaN).
-                    float mx[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            mx[c & 7] = max_nan(mx[c & 7], __uint_as_float(s[q][c]));
-                    const float tmax = sl2 * max_nan(max_nan(max_nan(mx[0], mx[1]),
-                                                             max_nan(mx[2], mx[3])),
-                                                     max_nan(max_nan(mx[4], mx[5]),
-                                                             max_nan(mx[6], mx[7])));
-                    // Lazy rescale: m moves only when a tile raises it by more than 8.
-                    float alpha = 1.f;
-                    const bool raise = !(tmax <= m + 8.f);
-                    if (raise) {
-                        alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
-                        m = tmax;
-                    }
-                    // S_i came after P_i-2 V in the tensor pipe: O_t is at rest.
-                    if (i >= 2 && __any_sync(0xffffffffu, raise)) {
+                const int key0 = (kj - r.ctx_tiles) * kKeys;       // first drafted key (tree)
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            const uint32_t t_o = t_lanes + kOBase + t * D + c * 32;
-                            tmem_ld_32x32b_x32(t_o, o);
-                            tmem_wait_ld_dep(o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st_32x32b_x32(t_o, o);
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const uint64_t sl2x2 = f2(sl2, sl2), nmu2 = f2(-mu, -mu);
-                    uint64_t ps2[4] = {0, 0, 0, 0};
-                    // P takes the first 64 columns of S, two keys per column.
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t hp[16];
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const uint64_t a2 = ffma2(f2(__uint_as_float(s[q][c]),
-                                                         __uint_as_float(s[q][c + 1])),
-                                                      sl2x2, nmu2);
-                            float a0, a1;
-                            f2split(a2, a0, a1);
-                            const float e0 = ex2(a0), e1 = ex2(a1);
-                            ps2[(c >> 1) & 3] = fadd2(ps2[(c >> 1) & 3], f2(e0, e1));
-                            hp[c >> 1] = pack2<BF16>(e0, e1);
-                        }
-                        tmem_st_32x32b_x16(t_s + q * 16, hp);
-                    }
-                    float q0, q1, q2, q3;
-                    f2split(fadd2(ps2[0], ps2[1]), q0, q1);
-                    f2split(fadd2(ps2[2], ps2[3]), q2, q3);
-                    l = fmaf(l, alpha, (q0 + q1) + (q2 + q3));
-                    tmem_wait_st();
-                }
-                if (edge && (!two || t == 0)) {
-                    // Values of this tile that no row may meet, see the head of
-                    // the file.  Thread r looks after key r.
-                    const uint32_t item = j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2;
-                    const uint32_t st = item % NS;
-                    if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeSoftmax)) {
+                for (int h = 0; h < (lim > kHalf ? 2 : 1); ++h) {
+                    if (!wait_all(&s_full[2 * t + h], (s_phase >> h) & 1, kErrTreeSoftmax)) {
                         ok = false;
                         break;
                     }
-                    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-                    uint8_t *vrow = smem + S::kKVOff + st * S::kTileBytes + row * 128;
-                    bool odd = false;
+                    s_phase ^= 1u << h;
+                    tc_fence_after_sync();
+                    if (act) {
+                        const uint32_t t_h = t_s + h * kHalf;
+                        uint32_t s[2][32];
+                        tmem_ld_32x32b_x32(t_h, s[0]);
+                        tmem_ld_32x32b_x32(t_h + 32u, s[1]);
+                        tmem_wait_ld_dep(s[0]);
+                        tmem_wait_ld_dep(s[1]);
+                        if (edge) {
+                            // Visible columns: keys that exist, and for drafted ones
+                            // the row's mask (or, without one, keys up to its own).
+                            const int lim_row = tree && !mrow ? min(lim, tok + 1 - key0) : lim;
 #pragma unroll
-                    for (int a = 0; a < S::kAtoms; ++a)
+                            for (int q = 0; q < 2; ++q) {
+                                const int v = lim_row - h * kHalf - 32 * q;
+                                uint32_t vis =
+                                    v >= 32 ? 0xffffffffu : (v <= 0 ? 0u : (1u << v) - 1u);
+                                if (tree && mrow) {
+                                    const int w = (key0 >> 5) + 2 * h + q;
+                                    vis &= row < rows && w < p.words
+                                               ? static_cast<uint32_t>(mrow[w])
+                                               : 0u;
+                                }
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(vrow + a * kAtomBytes +
-                                                                  (((c + row) & 7) << 4));
+                                for (int c = 0; c < 32; ++c)
+                                    if (!((vis >> c) & 1u)) s[q][c] = __float_as_uint(-INFINITY);
+                            }
+                        }
+                        // The maximum keeps NaN (a NaN score makes the row NaN).
+                        float mx[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            mx[u] = max_nan(__uint_as_float(s[0][u]), __uint_as_float(s[1][u]));
+#pragma unroll
+                        for (int c = 4; c < 32; ++c)
+                            mx[c & 3] = max3_nan(mx[c & 3], __uint_as_float(s[0][c]),
+                                                 __uint_as_float(s[1][c]));
+                        const float tmax =
+                            sl2 * max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+                        // Lazy rescale: m moves only when a half raises it by more than 8.
+                        float alpha = 1.f;
+                        const bool raise = !(tmax <= m + 8.f);
+                        if (raise) {
+                            alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
+                            m = tmax;
+                        }
+                        if (done != pv && __any_sync(0xffffffffu, raise)) {
+                            if (!wait_pv(done - 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                const uint32_t t_o = t_lanes + kOBase + t * D + c * 32;
+                                tmem_ld_32x32b_x32(t_o, o);
+                                tmem_wait_ld_dep(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st_32x32b_x32(t_o, o);
+                            }
+                        }
+                        const float mu = m == -INFINITY ? 0.f : m;
+                        const uint64_t sl2x2 = f2(sl2, sl2), nmu2 = f2(-mu, -mu);
+                        uint64_t ps2[4] = {0, 0, 0, 0};
+                        // P takes the first 32 columns of S, two keys per column.
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t hp[16];
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const uint64_t a2 = ffma2(f2(__uint_as_float(s[q][c]),
+                                                             __uint_as_float(s[q][c + 1])),
+                                                          sl2x2, nmu2);
+                                float a0, a1;
+                                f2split(a2, a0, a1);
+                                const float e0 = ex2(a0), e1 = ex2(a1);
+                                ps2[(c >> 1) & 3] = fadd2(ps2[(c >> 1) & 3], f2(e0, e1));
+                                hp[c >> 1] = pack2<BF16>(e0, e1);
+                            }
+                            tmem_st_32x32b_x16(t_h + q * 16, hp);
+                        }
+                        float q0, q1, q2, q3;
+                        f2split(fadd2(ps2[0], ps2[1]), q0, q1);
+                        f2split(fadd2(ps2[2], ps2[3]), q2, q3);
+                        l = fmaf(l, alpha, (q0 + q1) + (q2 + q3));
+                        tmem_wait_st();
+                    }
+                    ++done;
+                    if (edge && h == 0 && (!two || t == 0)) {
+                        // Values of this tile that no row may meet, see the head of
+                        // the file.  Thread r looks after key r.
+                        const uint32_t item = j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2;
+                        const uint32_t st = item % NS;
+                        if (!wait_all(&kv_full[st], (item / NS) & 1, kErrTreeSoftmax)) {
+                            ok = false;
+                            break;
+                        }
+                        constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+                        uint8_t *vrow = smem + S::kKVOff + st * S::kTileBytes + row * 128;
+                        bool odd = false;
+#pragma unroll 4
+                        for (int a = 0; a < S::kAtoms * 8; ++a) {
+                            // 16 bytes of the row at a time, each lane from another place on
+                            uint4 *at = reinterpret_cast<uint4 *>(vrow + (a >> 3) * kAtomBytes +
+                                                                  (((a + row) & 7) << 4));
                             if (row >= lim) {
                                 *at = make_uint4(0, 0, 0, 0);
                             } else if (tree) {
@@ -692,27 +783,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                         }
-                    if (odd) *odd_values = 1;
-                    fence_proxy_async_smem();     // the tensor core reads the tile next
+                        if (odd) *odd_values = 1;
+                        fence_proxy_async_smem();     // the tensor core reads the tile next
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
             // End of the part.  A single query tile: both groups' outputs are
             // joined, each group doing half of the columns.
-            const int other_steps = N > 1 ? 1 : 0;     // group 1 had steps
-            if (!two || t == 0)
-                ok = wait_all(&o_full[0], outs[0] & 1, kErrTreeSoftmax);
-            if (ok && other_steps && (!two || t == 1))
-                ok = wait_all(&o_full[1], outs[1] & 1, kErrTreeSoftmax);
-            if (!ok) break;
-            ++outs[0];
-            outs[1] += other_steps;
+            const bool second = N > 1;     // group 1 had steps
+            if (done != pv && !wait_pv(done - 1)) break;
+            pv = done;
             float w0 = t == 0 ? 1.f : 0.f, w1 = t == 1 ? 1.f : 0.f;
             if (!two) {
+                // The previous part's m and l have been read by both groups.
+                if (parts > 0 && !wait_all(o_free, (parts - 1) & 1, kErrTreeSoftmax)) {
+                    ok = false;
+                    break;
+                }
                 ml[t * kRows + row] = make_float2(m, l);
+                tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ml_full);
                 if (!wait_all(ml_full, joins & 1, kErrTreeSoftmax)) {
@@ -726,12 +819,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w1 = b.x == -INFINITY ? 0.f : ex2(b.x - m);
                 l = fmaf(a.y, w0, b.y * w1);
             }
+            ++parts;
             tc_fence_after_sync();
             if (act) {
                 const bool whole = walk.whole();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const int c_lo = two ? 0 : t * (D / 64), c_hi = two ? D / 32 : c_lo + D / 64;
-                const int hd = row - tl * p.group;
                 uint16_t *orow = p.out + grow * p.out_token_stride +
                                  static_cast<int64_t>(walk.head * p.group + hd) *
                                      p.out_head_stride;
@@ -744,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t o[32];
                     float x[32];
-                    if (two || other_steps) {
+                    if (two || second) {
                         const int g = two ? t : 1;
                         tmem_ld_32x32b_x32(t_lanes + kOBase + g * D + c * 32, o);
                         tmem_wait_ld_dep(o);
@@ -829,33 +922,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the units that more than one CTA worked on:
 //   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s.
-// Block (c, y): the unit that began in CTA c's share, columns [8 y, 8 y + 8) of
-// both query tiles.  A block's threads are `rp` rows (a power of two that
-// covers the rows in use) times 512 / rp groups of parts, whose sums are added
-// up in order.  Bound by the latency of the partial results' loads (they lie
-// in L2); hence the many groups where there are few rows.
+// Block (c, y): the unit that began in CTA c's share, columns [32 y, 32 y + 32)
+// of both query tiles.  A thread has 8 columns of a row for one of `groups` runs
+// of parts; rp (a power of two that covers the rows in use) x 4 x groups
+// threads, and the groups' sums are added up in order.  Bound by the latency of
+// the partial results' loads (they lie in L2); hence the many groups where
+// there are few rows.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinCols = 32;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p)
 {
     using S = TreeShape<D>;
-    __shared__ float s_acc[kJoinThreads][9];      // 8 columns and the sum
+    __shared__ float s_acc[9][kJoinThreads];      // 8 columns and the sum
     __shared__ float s_max[kJoinThreads];
-    const int c = blockIdx.x, col0 = blockIdx.y * 8, tid = threadIdx.x;
+    const int c = blockIdx.x, tid = threadIdx.x;
     grid_dependency_wait();
     const Split sp = p.split[c];
     if (sp.ctas < 2) return;
-    const Request r = request(p, sp.b);
-    const int head = sp.unit / r.pairs, pair = sp.unit - head * r.pairs;
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-        const int tok0 = (2 * pair + t) * p.tile_tokens;
-        const int rows = min(p.tile_tokens, r.n - tok0) * p.group;
+        const int rows = sp.rows[t];
         if (rows <= 0) break;
-        int rp = 8;
-        while (rp < rows) rp <<= 1;
-        const int groups = kJoinThreads / rp;
-        const int row = tid & (rp - 1), g = tid / rp;
+        int shift = 3;
+        while ((1 << shift) < rows) ++shift;
+        const int rp = 1 << shift;
+        const int row = tid & (rp - 1), cg = (tid >> shift) & 3, g = tid >> (shift + 2);
+        const int groups = kJoinThreads >> (shift + 2);
+        const int col0 = blockIdx.y * kJoinCols + cg * 8;
         const int per = (sp.ctas + groups - 1) / groups;
         const int s0 = min(g * per, sp.ctas), s1 = min(s0 + per, sp.ctas);
         // Part s lies in CTA c + s: the one that begins a unit, then first parts.
@@ -868,7 +963,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
             for (int s = s0; s < s1; ++s) mx = fmaxf(mx, __ldcg(slot(s) + D * kRows));
         s_max[tid] = mx;
         __syncthreads();
-        for (int i = 0; i < groups; ++i) mx = fmaxf(mx, s_max[i * rp + row]);
+        for (int i = 0; i < groups; ++i) mx = fmaxf(mx, s_max[((i * 4 + cg) << shift) + row]);
         float acc[9];
 #pragma unroll
         for (int e = 0; e < 9; ++e) acc[e] = 0.f;
@@ -883,12 +978,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
                 acc[8] = fmaf(__ldcg(part + (D + 1) * kRows), w, acc[8]);
             }
 #pragma unroll
-        for (int e = 0; e < 9; ++e) s_acc[tid][e] = acc[e];
+        for (int e = 0; e < 9; ++e) s_acc[e][tid] = acc[e];
         __syncthreads();
         if (g == 0 && row < rows) {
             for (int i = 1; i < groups; ++i)
 #pragma unroll
-                for (int e = 0; e < 9; ++e) acc[e] += s_acc[i * rp + row][e];
+                for (int e = 0; e < 9; ++e) acc[e] += s_acc[e][((i * 4 + cg) << shift) + row];
             const float inv = acc[8] > 0.f ? 1.f / acc[8] : 0.f;
             const int tl = row / p.group, hd = row - tl * p.group;
             uint4 u;
@@ -897,8 +992,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
             u.z = pack2<BF16>(acc[4] * inv, acc[5] * inv);
             u.w = pack2<BF16>(acc[6] * inv, acc[7] * inv);
             *reinterpret_cast<uint4 *>(
-                p.out + (static_cast<int64_t>(r.s0) + tok0 + tl) * p.out_token_stride +
-                static_cast<int64_t>(head * p.group + hd) * p.out_head_stride + col0) = u;
+                p.out +
+                (static_cast<int64_t>(sp.first) + t * p.tile_tokens + tl) * p.out_token_stride +
+                static_cast<int64_t>(sp.head * p.group + hd) * p.out_head_stride + col0) = u;
         }
         __syncthreads();
     }
@@ -963,7 +1059,7 @@ tg_status_t launch(const Maps &maps, const tgt::TreeParams &p, int grid, cudaStr
         maps.q, maps.kc, maps.vc, maps.k, maps.v, p);
     if (cudaGetLastError() != cudaSuccess) return TG_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, D / 8);
+    cfg.gridDim = dim3(grid, D / tgt::kJoinCols);
     cfg.blockDim = dim3(tgt::kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
