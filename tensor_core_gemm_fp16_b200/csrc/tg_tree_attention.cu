@@ -17,7 +17,7 @@
 // parts of a divided one leave their unnormalised output, maxima and sums in
 // the workspace, and a second kernel joins them in the CTAs' order.
 //
-// One CTA per SM, ten warps:
+// One CTA per SM, twelve warps:
 //   warps 0-3, 4-7  two softmax groups, thread r of a group owns query row r
 //                   (TMEM lane r).  A unit with two query tiles gives one to
 //                   each group, both over all key tiles; a unit with one gives
@@ -25,8 +25,11 @@
 //                   other the odd ones, each with its own maximum, sum and
 //                   output, joined at the end in tensor memory.  Either way
 //                   one group's exponentials run beside the other's products.
-//   warp 8          TMA producer: queries, and keys and values through one
-//                   ring in the order in which the products need them.
+//   warps 8, 10, 11 TMA producers: queries, and keys and values through one
+//                   ring in the order in which the products need them, each
+//                   a third of a tile's pages (a warp needs about 100 cycles
+//                   per copy; with pages of 16 tokens one alone held the
+//                   stream of 64 requests to 4.0 TB/s, three give 5.4).
 //   warp 9          TMEM allocator and MMA issuer.
 // Step i (a key tile of a query tile) belongs to group t = i mod 2 and has two
 // halves of 64 keys, each with its own score columns.  The issuer's order is
@@ -71,7 +74,8 @@ constexpr int kAtom = 64;          // head-dim elements per 128-byte swizzle ato
 constexpr int kAtomBytes = 128 * 128;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kWarps = 10;
+constexpr int kWarps = 12;
+constexpr int kProducers = 3;      // warps 8, 10 and 11
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOBase = 256;
@@ -411,38 +415,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, ok);
     };
 
-    if (warp == kProducerWarp) {
+    if (warp == kProducerWarp || warp > kMmaWarp) {
+        // Producer `me` of kProducers; the first one also announces the bytes.
+        const int me = warp == kProducerWarp ? 0 : warp - kMmaWarp;
         uint32_t qc = 0, ic = 0;       // query tiles and ring items so far
         bool ok = true;
         const int shift = p.page_shift;
         const bool small = shift < 7;                     // pages of less than a tile
         const int per_tile = small ? kKeys >> shift : 1;  // pages of a tile
-        const int my_page = lane / S::kAtoms, my_atom = lane % S::kAtoms;
-        const uint32_t my_off = my_atom * kAtomBytes + (small ? my_page << (shift + 7) : 0);
         while (ok && walk.next(p, lane)) {
             const Request &r = walk.r;
             for (int t = 0; t < (walk.two ? 2 : 1) && ok; ++t, ++qc) {
                 const uint32_t slot = qc & 1u;
                 if (qc >= 2) ok = wait_all(&q_empty[slot], ((qc >> 1) - 1) & 1, kErrTreeProducer);
                 if (!ok) break;
-                if (lane == 0)
+                if (me == 0 && elect_lane()) {
                     mbar_arrive_expect_tx(&q_full[slot],
                                           p.group * p.tile_tokens * S::kAtoms * 128);
+#pragma unroll
+                    for (int a = 0; a < S::kAtoms; ++a)
+                        tma_load_3d(sbase + S::kQOff + slot * S::kTileBytes + a * kAtomBytes, &tmQ,
+                                    &q_full[slot], a * kAtom, walk.head * p.group,
+                                    r.s0 + (2 * walk.pair + t) * p.tile_tokens);
+                }
                 __syncwarp();
-                if (lane < S::kAtoms)
-                    tma_load_3d(sbase + S::kQOff + slot * S::kTileBytes + lane * kAtomBytes, &tmQ,
-                                &q_full[slot], lane * kAtom, walk.head * p.group,
-                                r.s0 + (2 * walk.pair + t) * p.tile_tokens);
             }
             const int n = walk.k1 - walk.k0;
             const int32_t *table = p.tables + static_cast<int64_t>(walk.b) * p.table_stride;
-            // This lane's page of key tile kj of the cache (-1: none).
+            // Lane i: page i of key tile kj of the cache (-1: none).
             auto page_of = [&](int kj) -> int {
-                if (kj >= r.ctx_tiles || my_page >= per_tile) return -1;
-                const int pi = small ? kj * per_tile + my_page : (kj * kKeys) >> shift;
+                if (kj >= r.ctx_tiles || lane >= per_tile) return -1;
+                const int pi = small ? kj * per_tile + lane : (kj * kKeys) >> shift;
                 return (static_cast<int64_t>(pi) << shift) < r.ctx ? table[pi] : -1;
             };
-            // Page entries outside the cache read as zeros (out of the map's range).
+            // One elected thread issues (with coordinates of its own, each lane's
+            // copy would be issued by itself, several times slower).  Page entries
+            // outside the cache read as zeros (out of the map's range).
             auto load = [&](int kj, int page, bool value) {
                 const uint32_t st = ic % NS;
                 const uint32_t dst = sbase + S::kKVOff + st * S::kTileBytes;
@@ -452,20 +460,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pages =
                         small ? min(per_tile, (left + (1 << shift) - 1) >> shift) : 1;
                     const int rows = small ? pages << shift : kKeys;
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
-                    __syncwarp();
-                    if (my_page < pages && !skip)
-                        tma_load_4d(dst + my_off, value ? &tmVC : &tmKC, &kv_full[st],
-                                    my_atom * kAtom,
-                                    small ? 0 : (kj * kKeys) & ((1 << shift) - 1), walk.head,
-                                    page);
-                } else {
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], S::kTileBytes);
-                    __syncwarp();
-                    if (lane < S::kAtoms && !skip)
-                        tma_load_3d(dst + lane * kAtomBytes, value ? &tmV : &tmK, &kv_full[st],
-                                    lane * kAtom, r.s0 + (kj - r.ctx_tiles) * kKeys, walk.head);
+                    const int y = small ? 0 : (kj * kKeys) & ((1 << shift) - 1);
+                    const CUtensorMap *map = value ? &tmVC : &tmKC;
+                    if (me == 0 && elect_lane())
+                        mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
+                    for (int i = me; i < pages; i += kProducers) {
+                        const int id = __shfl_sync(0xffffffffu, page, i);
+                        if (elect_lane() && !skip)
+#pragma unroll
+                            for (int a = 0; a < S::kAtoms; ++a)
+                                tma_load_4d(dst + a * kAtomBytes + (i << (shift + 7)), map,
+                                            &kv_full[st], a * kAtom, y, walk.head, id);
+                    }
+                } else if (me == 0 && elect_lane()) {
+                    mbar_arrive_expect_tx(&kv_full[st], S::kTileBytes);
+                    const CUtensorMap *map = value ? &tmV : &tmK;
+                    if (!skip)
+#pragma unroll
+                        for (int a = 0; a < S::kAtoms; ++a)
+                            tma_load_3d(dst + a * kAtomBytes, map, &kv_full[st], a * kAtom,
+                                        r.s0 + (kj - r.ctx_tiles) * kKeys, walk.head);
                 }
+                __syncwarp();
                 ++ic;
             };
             // Items K_0 | K_1 V_0 | K_2 V_1 | ... | V_n-1; the next tile's page
@@ -492,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Every copy lands before shared memory goes away (the injected test
         // skips one load, whose barrier never completes).
-        if (lane == 0) {
+        if (me == 0 && lane == 0) {
             for (uint32_t s = 0; s < 2; ++s)
                 if (qc > s && !mbar_wait_drain(&q_full[s], ((qc - 1 - s) >> 1) & 1, limit))
                     atomicOr(p.error_word, kErrTreeDrain);
