@@ -652,6 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t grow = static_cast<int64_t>(r.s0) + tok;
             const int32_t *mrow = p.mask ? p.mask + grow * p.mask_stride : nullptr;
             uint32_t done = pv;     // products of this group before the next
+            // The row's mask words for the first tile of drafted keys, fetched ahead.
+            uint32_t bits[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                bits[q] = mrow && row < rows && q < p.words ? static_cast<uint32_t>(mrow[q]) : 0u;
             float m = -INFINITY;    // running maximum of the scaled scores, log2 units
             float l = 0.f;          // running sum of 2^(score - m)
             for (int i = t; ok && i < N; i += 2) {
@@ -687,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     v >= 32 ? 0xffffffffu : (v <= 0 ? 0u : (1u << v) - 1u);
                                 if (tree && mrow) {
                                     const int w = (key0 >> 5) + 2 * h + q;
-                                    vis &= row < rows && w < p.words
+                                    vis &= key0 == 0 ? (h ? bits[2 + q] : bits[q])
+                                           : row < rows && w < p.words
                                                ? static_cast<uint32_t>(mrow[w])
                                                : 0u;
                                 }
@@ -768,38 +774,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
-                        constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
                         uint8_t *vrow = smem + S::kKVOff + st * S::kTileBytes + row * 128;
-                        bool odd = false;
-#pragma unroll 4
-                        for (int a = 0; a < S::kAtoms * 8; ++a) {
-                            // 16 bytes of the row at a time, each lane from another place on
-                            uint4 *at = reinterpret_cast<uint4 *>(vrow + (a >> 3) * kAtomBytes +
-                                                                  (((a + row) & 7) << 4));
-                            if (row >= lim) {
-                                *at = make_uint4(0, 0, 0, 0);
-                            } else if (tree) {
-                                uint4 x = *at;
-                                uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                                bool hit = false;
+                        if (row >= lim) {
+                            if (lim > kHalf || row < kHalf)      // else no product reads it
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((w[e] & kExp) == kExp) {
-                                        w[e] &= 0xFFFF0000u;
-                                        hit = true;
-                                    }
-                                    if ((w[e] & (kExp << 16)) == (kExp << 16)) {
-                                        w[e] &= 0x0000FFFFu;
-                                        hit = true;
-                                    }
-                                }
-                                if (hit) {
-                                    *at = x;
-                                    odd = true;
+                                for (int a = 0; a < S::kAtoms * 8; ++a)
+                                    *reinterpret_cast<uint4 *>(vrow + (a >> 3) * kAtomBytes +
+                                                               (((a + row) & 7) << 4)) =
+                                        make_uint4(0, 0, 0, 0);
+                        } else if (tree) {
+                            // An exponent of all ones carries into the sign's place.
+                            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u;
+                            constexpr uint32_t kOne = BF16 ? 0x00800080u : 0x04000400u;
+                            uint32_t odd = 0;
+#pragma unroll 8
+                            for (int a = 0; a < S::kAtoms * 8; ++a) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(
+                                    vrow + (a >> 3) * kAtomBytes + (((a + row) & 7) << 4));
+                                odd |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) |
+                                       ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+                            }
+                            if (odd & 0x80008000u) {
+                                *odd_values = 1;
+#pragma unroll 1
+                                for (int a = 0; a < S::kAtoms * 32; ++a) {
+                                    uint32_t *w = reinterpret_cast<uint32_t *>(
+                                        vrow + (a >> 5) * kAtomBytes + (a & 31) * 4);
+                                    const uint32_t hit = ((*w & kExp) + kOne) & 0x80008000u;
+                                    if (hit & 0x00008000u) *w &= 0xFFFF0000u;
+                                    if (hit & 0x80000000u) *w &= 0x0000FFFFu;
                                 }
                             }
                         }
-                        if (odd) *odd_values = 1;
                         fence_proxy_async_smem();     // the tensor core reads the tile next
                     }
                     tc_fence_before_sync();
@@ -938,81 +944,85 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the units that more than one CTA worked on:
 //   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s.
-// Block (c, y): the unit that began in CTA c's share, columns [32 y, 32 y + 32)
-// of both query tiles.  A thread has 8 columns of a row for one of `groups` runs
-// of parts; rp (a power of two that covers the rows in use) x 4 x groups
-// threads, and the groups' sums are added up in order.  Bound by the latency of
-// the partial results' loads (they lie in L2); hence the many groups where
-// there are few rows.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinCols = 32;
+// Block (c, y): the unit that began in CTA c's share, 16 columns of one of its
+// query tiles.  A thread has 8 columns of a row for one of `groups` runs of
+// parts, in one pass with a running maximum: rp (a power of two that covers the
+// rows in use) x 2 x groups threads.  The groups are then joined in order
+// through shared memory.  Bound by the latency of the partial results' loads
+// (they lie in L2), hence the single pass, and the many groups where there are
+// few rows.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 16;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p)
 {
     using S = TreeShape<D>;
-    __shared__ float s_acc[9][kJoinThreads];      // 8 columns and the sum
-    __shared__ float s_max[kJoinThreads];
+    __shared__ float s_part[10][kJoinThreads];      // 8 columns, maximum and sum
     const int c = blockIdx.x, tid = threadIdx.x;
+    const int t = static_cast<int>(blockIdx.y) / (D / kJoinCols);
+    const int col0 = (static_cast<int>(blockIdx.y) % (D / kJoinCols)) * kJoinCols;
     grid_dependency_wait();
-    const Split sp = p.split[c];
-    if (sp.ctas < 2) return;
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-        const int rows = sp.rows[t];
-        if (rows <= 0) break;
-        int shift = 3;
-        while ((1 << shift) < rows) ++shift;
-        const int rp = 1 << shift;
-        const int row = tid & (rp - 1), cg = (tid >> shift) & 3, g = tid >> (shift + 2);
-        const int groups = kJoinThreads >> (shift + 2);
-        const int col0 = blockIdx.y * kJoinCols + cg * 8;
-        const int per = (sp.ctas + groups - 1) / groups;
-        const int s0 = min(g * per, sp.ctas), s1 = min(s0 + per, sp.ctas);
-        // Part s lies in CTA c + s: the one that begins a unit, then first parts.
-        auto slot = [&](int s) {
-            return p.part +
-                   (static_cast<int64_t>(c + s) * 4 + (s == 0 ? 2 : 0) + t) * S::kPartFloats + row;
-        };
-        float mx = -INFINITY;
-        if (row < rows)
-            for (int s = s0; s < s1; ++s) mx = fmaxf(mx, __ldcg(slot(s) + D * kRows));
-        s_max[tid] = mx;
-        __syncthreads();
-        for (int i = 0; i < groups; ++i) mx = fmaxf(mx, s_max[((i * 4 + cg) << shift) + row]);
-        float acc[9];
+    const Split *sp = p.split + c;
+    const int ctas = sp->ctas, head = sp->head, first = sp->first, rows = sp->rows[t];
+    if (ctas < 2 || rows <= 0) return;
+    const int shift = rows <= 8 ? 3 : 32 - __clz(rows - 1);
+    const int row = tid & ((1 << shift) - 1), cg = (tid >> shift) & 1, g = tid >> (shift + 1);
+    const int groups = kJoinThreads >> (shift + 1);
+    const int per = (ctas + groups - 1) / groups;
+    const int s0 = min(g * per, ctas), s1 = min(s0 + per, ctas);
+    float m = -INFINITY, acc[9];
 #pragma unroll
-        for (int e = 0; e < 9; ++e) acc[e] = 0.f;
-        if (row < rows)
-            for (int s = s0; s < s1; ++s) {
-                const float *part = slot(s);
-                const float ms = __ldcg(part + D * kRows);
-                const float w = ms == -INFINITY ? 0.f : ex2(ms - mx);
+    for (int e = 0; e < 9; ++e) acc[e] = 0.f;
+    if (row < rows) {
+#pragma unroll 2
+        for (int s = s0; s < s1; ++s) {
+            // Part s lies in CTA c + s: the one that begins a unit, then first parts.
+            const float *part =
+                p.part +
+                (static_cast<int64_t>(c + s) * 4 + (s == 0 ? 2 : 0) + t) * S::kPartFloats + row;
+            const float ms = __ldcg(part + D * kRows), ls = __ldcg(part + (D + 1) * kRows);
+            float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    acc[e] = fmaf(__ldcg(part + (col0 + e) * kRows), w, acc[e]);
-                acc[8] = fmaf(__ldcg(part + (D + 1) * kRows), w, acc[8]);
-            }
+            for (int e = 0; e < 8; ++e) x[e] = __ldcg(part + (col0 + cg * 8 + e) * kRows);
+            const float mn = max_nan(m, ms);
+            const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
+            const float w1 = ms == -INFINITY ? 0.f : ex2(ms - mn);
+            m = mn;
 #pragma unroll
-        for (int e = 0; e < 9; ++e) s_acc[e][tid] = acc[e];
-        __syncthreads();
-        if (g == 0 && row < rows) {
-            for (int i = 1; i < groups; ++i)
-#pragma unroll
-                for (int e = 0; e < 9; ++e) acc[e] += s_acc[e][((i * 4 + cg) << shift) + row];
-            const float inv = acc[8] > 0.f ? 1.f / acc[8] : 0.f;
-            const int tl = row / p.group, hd = row - tl * p.group;
-            uint4 u;
-            u.x = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-            u.y = pack2<BF16>(acc[2] * inv, acc[3] * inv);
-            u.z = pack2<BF16>(acc[4] * inv, acc[5] * inv);
-            u.w = pack2<BF16>(acc[6] * inv, acc[7] * inv);
-            *reinterpret_cast<uint4 *>(
-                p.out +
-                (static_cast<int64_t>(sp.first) + t * p.tile_tokens + tl) * p.out_token_stride +
-                static_cast<int64_t>(sp.head * p.group + hd) * p.out_head_stride + col0) = u;
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(x[e], w1, acc[e] * w0);
+            acc[8] = fmaf(ls, w1, acc[8] * w0);
         }
+    }
+    if (groups > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_part[e][tid] = acc[e];
+        s_part[8][tid] = acc[8];
+        s_part[9][tid] = m;
         __syncthreads();
+        if (g > 0) return;
+        for (int i = 1; i < groups; ++i) {
+            const int o = (i << (shift + 1)) + tid;
+            const float ms = s_part[9][o];
+            const float mn = max_nan(m, ms);
+            const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
+            const float w1 = ms == -INFINITY ? 0.f : ex2(ms - mn);
+            m = mn;
+#pragma unroll
+            for (int e = 0; e < 9; ++e) acc[e] = fmaf(s_part[e][o], w1, acc[e] * w0);
+        }
+    }
+    if (row < rows) {
+        const float inv = acc[8] > 0.f ? 1.f / acc[8] : 0.f;
+        const int tl = row / p.group, hd = row - tl * p.group;
+        uint4 u;
+        u.x = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+        u.y = pack2<BF16>(acc[2] * inv, acc[3] * inv);
+        u.z = pack2<BF16>(acc[4] * inv, acc[5] * inv);
+        u.w = pack2<BF16>(acc[6] * inv, acc[7] * inv);
+        *reinterpret_cast<uint4 *>(
+            p.out + (static_cast<int64_t>(first) + t * p.tile_tokens + tl) * p.out_token_stride +
+            static_cast<int64_t>(head * p.group + hd) * p.out_head_stride + col0 + cg * 8) = u;
     }
 }
 
@@ -1075,7 +1085,7 @@ tg_status_t launch(const Maps &maps, const tgt::TreeParams &p, int grid, cudaStr
         maps.q, maps.kc, maps.vc, maps.k, maps.v, p);
     if (cudaGetLastError() != cudaSuccess) return TG_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, D / tgt::kJoinCols);
+    cfg.gridDim = dim3(grid, 2 * (D / tgt::kJoinCols));
     cfg.blockDim = dim3(tgt::kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
