@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import NamedTuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +99,12 @@ class tg_tree_attention_t(ctypes.Structure):
          ("inject", ctypes.c_int)]
 
 
+# The same struct as bytes: packing it takes a quarter of the time of setting 36 ctypes fields.
+_TREE_ARGS = struct.Struct("@" + "".join(
+    {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P",
+     ctypes.c_size_t: "N", ctypes.c_uint64: "Q"}[t] for _, t in tg_tree_attention_t._fields_)
+    + "0q")
+
 _lib = None
 
 
@@ -155,6 +162,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tg_tree_mask.restype = c_int
     lib.tg_tree_attention.argtypes = [ctypes.POINTER(tg_tree_attention_t), vp]
     lib.tg_tree_attention.restype = c_int
+    lib._tree_attention_packed = lib["tg_tree_attention"]      # the struct as bytes
+    lib._tree_attention_packed.argtypes = [ctypes.c_char_p, vp]
+    lib._tree_attention_packed.restype = c_int
     lib.tg_tree_attention_workspace_size.argtypes = [i64]
     lib.tg_tree_attention_workspace_size.restype = sz
     _lib = lib
@@ -435,74 +445,86 @@ class CachePlan(NamedTuple):
     status: "torch.Tensor"      # (1,) int32
 
 
-def _check(name, t, dtype, shape, device):
-    """An index tensor: its type, shape (None: any extent), device and contiguity."""
+def _refuse(name, t, dtype, shape, index):
+    """The error for a tensor that is not a contiguous ``dtype`` tensor of ``shape`` (None: any
+    extent) on CUDA device ``index``."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _table(name, t, rows, device):
-    """An int32 table whose rows are contiguous; returns its row stride."""
-    if t.dtype.itemsize != 4 or t.dtype.is_floating_point:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"{name} must have shape ({rows}, n), got {tuple(t.shape)}")
-    stride = t.stride(0) if rows > 1 else max(t.shape[1], 1)
-    if (t.shape[1] > 1 and t.stride(1) != 1) or stride < t.shape[1]:
+def _vector(name, t, dtype, n, index):
+    """Check a contiguous one-dimensional tensor of n elements; returns its address.  (These
+    checks are most of the time of a short call, hence one test of all that may be wrong.)"""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n,) \
+            or not t.is_contiguous():
+        _refuse(name, t, dtype, (n,), index)
+    return t.data_ptr()
+
+
+def _table(name, t, dtype, rows, index):
+    """Check an int32 table with contiguous rows; returns (address, row stride, columns)."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2 or t.shape[0] != rows:
+        _refuse(name, t, dtype, (rows, None), index)
+    cols, (row, col) = t.shape[1], t.stride()
+    if rows < 2:
+        row = max(cols, 1)
+    if (cols > 1 and col != 1) or row < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return stride
+    return t.data_ptr(), row, cols
 
 
-def _rows(name, t, dtype, heads, dim, device):
-    """A (tokens, heads, dim) tensor whose last dimension is contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+def _rows(name, t, dtype, shape, index):
+    """Check a (tokens, heads, dim) tensor whose last dimension is contiguous; returns its
+    strides."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        _refuse(name, t, dtype, shape, index)
+    strides = t.stride()
+    if strides[2] != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
+    return strides
 
 
-def _caches(k_cache, v_cache, dtype, device):
-    """Both caches: (pages, page size, heads, dim) tensors of the same shape and strides."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be (pages, page size, heads, dim) with a contiguous "
-                             "last dimension")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _caches(k_cache, v_cache, dtype, index):
+    """Check both caches: (pages, page size, heads, dim) tensors of the same shape and strides,
+    the last dimension contiguous; returns shape and strides."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4:
+        raise ValueError("k_cache must be (pages, page size, heads, dim)")
+    if k_cache.dtype is not dtype or k_cache.get_device() != index:
+        _refuse("k_cache", k_cache, dtype, shape, index)
+    if v_cache.dtype is not dtype or v_cache.get_device() != index:
+        _refuse("v_cache", v_cache, dtype, shape, index)
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if strides[3] != 1:
+        raise ValueError("the caches must have a contiguous last dimension")
+    return shape, strides
 
 
-def _call(torch, device, what, f, *args):
-    """Call a raw entry point on the device's current stream; raise on a non-OK status."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+def _device_index(name, t):
+    index = t.get_device() if t.is_cuda else -1
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _call(torch, index, what, f, *args):
+    """Call an entry point on the current stream of CUDA device ``index``; raise on a non-OK
+    status."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without a Stream object
+    stream = raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
         st = f(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = f(*args, stream)
     if st != TG_OK:
         raise TgError(st, what)
-
-
-def _cuda(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
 
 
 def cache_plan(lens, add, ring, free_pages, block_tables, page_size, tokens, *, starts=None,
@@ -518,32 +540,30 @@ def cache_plan(lens, add, ring, free_pages, block_tables, page_size, tokens, *, 
     (its six tensors) if given; with ``starts`` given, its starts are a copy.
     """
     import torch
-    dev = _cuda("lens", lens)
-    B, i32 = lens.shape[0] if lens.dim() else 0, torch.int32
-    for name, t, n in (("lens", lens, B), ("add", add, B), ("ring", ring, 2),
-                       ("free_pages", free_pages, None), ("starts", starts, B + 1),
-                       ("offsets", offsets, tokens)):
-        if t is not None:
-            _check(name, t, i32, (n,), dev)
-    stride = _table("block_tables", block_tables, B, dev)
+    index = _device_index("lens", lens)
+    B, i32 = lens.numel(), torch.int32
     if out is None:
         def new(n):
-            return torch.empty(n, dtype=i32, device=dev)
+            return torch.empty(n, dtype=i32, device=lens.device)
         out = CachePlan(new(B), new(2), new(B + 1),
-                        torch.empty(tokens, dtype=torch.int64, device=dev), new(tokens), new(1))
-    else:
+                        torch.empty(tokens, dtype=torch.int64, device=lens.device), new(tokens),
+                        new(1))
+    elif not isinstance(out, CachePlan):
         out = CachePlan(*out)
-        for name, t, n in (("out.lens", out.lens, B), ("out.ring", out.ring, 2),
-                           ("out.starts", out.starts, B + 1),
-                           ("out.positions", out.positions, tokens), ("out.status", out.status, 1)):
-            _check(name, t, i32, (n,), dev)
-        _check("out.slots", out.slots, torch.int64, (tokens,), dev)
-    _call(torch, dev, "tg_cache_plan", load().tg_cache_plan, lens.data_ptr(), add.data_ptr(), B,
-          starts.data_ptr() if starts is not None else None,
-          offsets.data_ptr() if offsets is not None else None, tokens, block_tables.data_ptr(),
-          stride, block_tables.shape[1], page_size, free_pages.data_ptr(), free_pages.shape[0],
-          ring.data_ptr(), out.lens.data_ptr(), out.ring.data_ptr(), out.starts.data_ptr(),
-          out.slots.data_ptr(), out.positions.data_ptr(), out.status.data_ptr())
+    pages = free_pages.numel()
+    table, stride, max_pages = _table("block_tables", block_tables, i32, B, index)
+    _call(torch, index, "tg_cache_plan", load().tg_cache_plan,
+          _vector("lens", lens, i32, B, index), _vector("add", add, i32, B, index), B,
+          None if starts is None else _vector("starts", starts, i32, B + 1, index),
+          None if offsets is None else _vector("offsets", offsets, i32, tokens, index), tokens,
+          table, stride, max_pages, page_size,
+          _vector("free_pages", free_pages, i32, pages, index), pages,
+          _vector("ring", ring, i32, 2, index), _vector("out.lens", out.lens, i32, B, index),
+          _vector("out.ring", out.ring, i32, 2, index),
+          _vector("out.starts", out.starts, i32, B + 1, index),
+          _vector("out.slots", out.slots, torch.int64, tokens, index),
+          _vector("out.positions", out.positions, i32, tokens, index),
+          _vector("out.status", out.status, i32, 1, index))
     return out
 
 
@@ -555,20 +575,17 @@ def cache_write(k, v, slots, k_cache, v_cache):
     128, any strides with a contiguous last dimension.  Returns the caches.
     """
     import torch
-    dev = _cuda("k", k)
-    if k.dtype.itemsize != 2:
-        raise TypeError(f"k must have a 16-bit type, got {k.dtype}")
-    _caches(k_cache, v_cache, k.dtype, dev)
-    pages, page, heads, dim = k_cache.shape
-    _rows("k", k, k.dtype, heads, dim, dev)
-    _rows("v", v, k.dtype, heads, dim, dev)
-    if k.shape != v.shape or k.stride() != v.stride():
-        raise ValueError("k and v must have the same shape and strides")
-    _check("slots", slots, torch.int64, (k.shape[0],), dev)
-    _call(torch, dev, "tg_cache_write", load().tg_cache_write, k.data_ptr(), v.data_ptr(),
-          k.shape[0], heads, dim, k.stride(0), k.stride(1), slots.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), pages, page, k_cache.stride(0), k_cache.stride(1),
-          k_cache.stride(2))
+    index, dt = _device_index("k", k), k.dtype
+    if dt.itemsize != 2:
+        raise TypeError(f"k must have a 16-bit type, got {dt}")
+    (pages, page, heads, dim), cs = _caches(k_cache, v_cache, dt, index)
+    n = k.shape[0] if k.dim() else 0
+    ks = _rows("k", k, dt, (n, heads, dim), index)
+    if _rows("v", v, dt, (n, heads, dim), index) != ks:
+        raise ValueError("k and v must have the same strides")
+    _call(torch, index, "tg_cache_write", load().tg_cache_write, k.data_ptr(), v.data_ptr(), n,
+          heads, dim, ks[0], ks[1], _vector("slots", slots, torch.int64, n, index),
+          k_cache.data_ptr(), v_cache.data_ptr(), pages, page, cs[0], cs[1], cs[2])
     return k_cache, v_cache
 
 
@@ -580,20 +597,21 @@ def tree_mask(parents, starts, words, out=None):
     if given.
     """
     import torch
-    dev = _cuda("parents", parents)
-    n, i32 = parents.shape[0] if parents.dim() else 0, torch.int32
-    _check("parents", parents, i32, (n,), dev)
-    _check("starts", starts, i32, (None,), dev)
-    if starts.shape[0] < 1:
+    index, n, i32 = _device_index("parents", parents), parents.numel(), torch.int32
+    batch = starts.numel() - 1
+    if batch < 0:
         raise ValueError("starts must have shape (batch + 1,)")
     if out is None:
-        out = (torch.empty((n, max(words, 0)), dtype=i32, device=dev),
-               torch.empty(n, dtype=i32, device=dev))
-    else:
-        _check("out[0]", out[0], i32, (n, words), dev)
-        _check("out[1]", out[1], i32, (n,), dev)
-    _call(torch, dev, "tg_tree_mask", load().tg_tree_mask, parents.data_ptr(), n,
-          starts.data_ptr(), starts.shape[0] - 1, words, out[0].data_ptr(), out[1].data_ptr())
+        out = (torch.empty((n, max(words, 0)), dtype=i32, device=parents.device),
+               torch.empty(n, dtype=i32, device=parents.device))
+    mask = out[0]
+    if mask.dtype is not i32 or mask.get_device() != index or mask.shape != (n, words) \
+            or not mask.is_contiguous():
+        _refuse("out[0]", mask, i32, (n, max(words, 0)), index)
+    _call(torch, index, "tg_tree_mask", load().tg_tree_mask,
+          _vector("parents", parents, i32, n, index), n,
+          _vector("starts", starts, i32, batch + 1, index), batch, words, mask.data_ptr(),
+          _vector("out[1]", out[1], i32, n, index))
     return out
 
 
@@ -612,48 +630,39 @@ def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=N
     are).
     """
     import torch
-    dev, dt = _cuda("q", q), q.dtype
-    if dt != torch.float16 and dt != torch.bfloat16:
+    index, dt = _device_index("q", q), q.dtype
+    if dt is not torch.float16 and dt is not torch.bfloat16:
         raise TypeError(f"q must be float16 or bfloat16, got {dt}")
-    _caches(k_cache, v_cache, dt, dev)
-    pages, page, kv_heads, dim = k_cache.shape
+    (pages, page, kv_heads, dim), cs = _caches(k_cache, v_cache, dt, index)
     if q.dim() != 3 or kv_heads < 1 or q.shape[1] % kv_heads:
         raise ValueError(f"q must have shape (tokens, a multiple of {kv_heads}, {dim}), got "
                          f"{tuple(q.shape)}")
-    n, heads = q.shape[0], q.shape[1]
-    _rows("q", q, dt, heads, dim, dev)
-    _rows("k", k, dt, kv_heads, dim, dev)
-    _rows("v", v, dt, kv_heads, dim, dev)
-    if k.shape[0] != n or v.shape[0] != n or (n and k.stride() != v.stride()):
-        raise ValueError("q, k and v must have the same number of rows, k and v the same strides")
-    B = lens.shape[0] if lens.dim() else 0
-    _check("lens", lens, torch.int32, (B,), dev)
-    _check("starts", starts, torch.int32, (B + 1,), dev)
-    stride = _table("block_tables", block_tables, B, dev)
-    words = mask_stride = 0
+    n, heads, _ = q.shape
+    qs = _rows("q", q, dt, (n, heads, dim), index)
+    ks = _rows("k", k, dt, (n, kv_heads, dim), index)
+    if _rows("v", v, dt, (n, kv_heads, dim), index) != ks:
+        raise ValueError("k and v must have the same strides")
+    B, i32 = lens.numel(), torch.int32
+    table, stride, max_pages = _table("block_tables", block_tables, i32, B, index)
+    bits, mask_stride, words = None, 0, 0
     if mask is not None:
-        mask_stride, words = _table("mask", mask, n, dev), mask.shape[1]
+        bits, mask_stride, words = _table("mask", mask, i32, n, index)
         if words < 1:
             raise ValueError("mask must have at least one word")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=dt, device=dev)
-    else:
-        _rows("out", out, dt, heads, dim, dev)
-        if out.shape[0] != n:
-            raise ValueError(f"out must have shape {(n, heads, dim)}")
+        out = q.new_empty((n, heads, dim))
+    os = _rows("out", out, dt, (n, heads, dim), index)
     if workspace is None:
-        workspace = torch.empty(tg_tree_attention_workspace_size(dim), dtype=torch.uint8,
-                                device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
-    args = tg_tree_attention_t(
-        TG_TYPE_BF16 if dt == torch.bfloat16 else TG_TYPE_FP16, n, B, kv_heads, heads // kv_heads,
-        dim, scale, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(),
-        k.stride(0), k.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
-        k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), block_tables.data_ptr(), stride,
-        block_tables.shape[1], lens.data_ptr(), starts.data_ptr(),
-        mask.data_ptr() if mask is not None else None, words, mask_stride, out.data_ptr(),
-        out.stride(0), out.stride(1), workspace.data_ptr(),
+        workspace = q.new_empty((tg_tree_attention_workspace_size(dim) + 1) // 2)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
+    args = _TREE_ARGS.pack(
+        TG_TYPE_BF16 if dt is torch.bfloat16 else TG_TYPE_FP16, n, B, kv_heads,
+        heads // kv_heads, dim, scale, q.data_ptr(), qs[0], qs[1], k.data_ptr(), v.data_ptr(),
+        ks[0], ks[1], k_cache.data_ptr(), v_cache.data_ptr(), pages, page, cs[0], cs[1], cs[2],
+        table, stride, max_pages, _vector("lens", lens, i32, B, index),
+        _vector("starts", starts, i32, B + 1, index), bits or 0, words, mask_stride,
+        out.data_ptr(), os[0], os[1], workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), wait_limit_ns, inject)
-    _call(torch, dev, "tg_tree_attention", load().tg_tree_attention, args)
+    _call(torch, index, "tg_tree_attention", load()._tree_attention_packed, args)
     return out

@@ -182,6 +182,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const CUtensorMap
         : "memory");
 }
 
+// a / b for a >= 0, b > 0.  A 64-bit division takes several hundred cycles and as
+// many instructions, which are kept out of the way.
+__device__ __noinline__ int64_t quotient64(int64_t a, int64_t b) { return a / b; }
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return quotient64(a, b);
+}
+
 // A request: its drafted rows, cached tokens, tiles and work.
 struct Request {
     int s0, n, ctx;      // first drafted row, drafted tokens, cached tokens
@@ -309,17 +319,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    // A thread's run of requests; the loads are on their way during the set-up.
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
+    int64_t work = 0;
+    for (int b = b0; b < b1; ++b) work += request(p, b).work;
+    if (threadIdx.x < S::kNumBars) {
+        uint64_t *bar = &bars[threadIdx.x];
+        const uint32_t count = (bar >= p_full && bar < pv_done)    ? 4u
+                               : (bar == o_free || bar == ml_full) ? 8u
+                                                                   : 1u;
+        mbar_init(bar, count);
+        fence_mbar_init();
+    }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kNumBars; ++i) {
-            uint64_t *bar = &bars[i];
-            const uint32_t count = (bar >= p_full && bar < pv_done)    ? 4u
-                                   : (bar == o_free || bar == ml_full) ? 8u
-                                                                       : 1u;
-            mbar_init(bar, count);
-        }
         *abort_flag = 0;
         *odd_values = 0;
-        fence_mbar_init();
     }
     if (warp == kProducerWarp && lane == 0) {
         tma_prefetch_desc(&tmQ);
@@ -333,17 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish<1>();
     }
 
-    // Share of this CTA: sums of the requests' work over the threads, each of
-    // which has a run of them.  Scratch in the ring, which is not in use yet.
+    // Share of this CTA, from the sums of the requests' work over the threads.
+    // Scratch in the ring, which is not in use yet.
     struct Scratch {
         int64_t sum[kWarps];
         Walk walk;
     };
     Scratch &scr = *reinterpret_cast<Scratch *>(smem + S::kKVOff);
-    const int per = (p.batch + kThreads - 1) / kThreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
-    int64_t work = 0;
-    for (int b = b0; b < b1; ++b) work += request(p, b).work;
     int64_t incl = work;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w < warp) hi += scr.sum[w];
         total += scr.sum[w];
     }
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t share = quotient(total + gridDim.x - 1, gridDim.x);
     const int64_t pos0 = min(total, cta * share);
     const int64_t pos1 = min(total, pos0 + share);
     if (pos0 == pos1 && threadIdx.x == 0) p.split[cta].ctas = 0;
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lo <= pos0 && pos0 < end) {
                 Walk w;
                 const int64_t rel = pos0 - lo;
-                const int unit = static_cast<int>(rel / r.nk);
+                const int unit = static_cast<int>(quotient(rel, r.nk));
                 w.left = pos1 - pos0;
                 w.b = b;
                 w.r = r;
@@ -383,11 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lo < pos1 && pos1 <= end) {
                 // The unit that holds the share's last key tile.
-                const int64_t u = (pos1 - 1 - lo) / r.nk;
+                const int64_t u = quotient(pos1 - 1 - lo, r.nk);
                 const int64_t ubegin = lo + u * r.nk, uend = ubegin + r.nk;
                 Split sp = {};
                 if (ubegin >= pos0 && uend > pos1)
-                    sp.ctas = static_cast<int>((uend - 1) / share) - cta + 1;
+                    sp.ctas = static_cast<int>(quotient(uend - 1, share)) - cta + 1;
                 sp.head = static_cast<int>(u) / r.pairs;
                 const int tok0 = 2 * (static_cast<int>(u) - sp.head * r.pairs) * p.tile_tokens;
                 sp.first = r.s0 + tok0;
@@ -425,6 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int per_tile = small ? kKeys >> shift : 1;  // pages of a tile
         while (ok && walk.next(p, lane)) {
             const Request &r = walk.r;
+            const int n = walk.k1 - walk.k0;
+            const int32_t *table = p.tables + static_cast<int64_t>(walk.b) * p.table_stride;
+            // Lane i: page i of key tile kj of the cache (-1: none).
+            auto page_of = [&](int kj) -> int {
+                if (kj >= r.ctx_tiles || lane >= per_tile) return -1;
+                const int pi = small ? kj * per_tile + lane : (kj * kKeys) >> shift;
+                return (static_cast<int64_t>(pi) << shift) < r.ctx ? table[pi] : -1;
+            };
+            int page_v = -1, page_k = page_of(walk.k0);
             for (int t = 0; t < (walk.two ? 2 : 1) && ok; ++t, ++qc) {
                 const uint32_t slot = qc & 1u;
                 if (qc >= 2) ok = wait_all(&q_empty[slot], ((qc >> 1) - 1) & 1, kErrTreeProducer);
@@ -440,14 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            const int n = walk.k1 - walk.k0;
-            const int32_t *table = p.tables + static_cast<int64_t>(walk.b) * p.table_stride;
-            // Lane i: page i of key tile kj of the cache (-1: none).
-            auto page_of = [&](int kj) -> int {
-                if (kj >= r.ctx_tiles || lane >= per_tile) return -1;
-                const int pi = small ? kj * per_tile + lane : (kj * kKeys) >> shift;
-                return (static_cast<int64_t>(pi) << shift) < r.ctx ? table[pi] : -1;
-            };
             // One elected thread issues (with coordinates of its own, each lane's
             // copy would be issued by itself, several times slower).  Page entries
             // outside the cache read as zeros (out of the map's range).
@@ -486,7 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // Items K_0 | K_1 V_0 | K_2 V_1 | ... | V_n-1; the next tile's page
             // entries are fetched while the ring has no room.
-            int page_v = -1, page_k = page_of(walk.k0);
             for (int t = 0; t < 2 * n && ok; ++t) {
                 if (ic >= NS)
                     ok = wait_all(&kv_empty[ic % NS], (ic / NS - 1) & 1, kErrTreeProducer);
