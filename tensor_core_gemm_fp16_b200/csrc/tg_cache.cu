@@ -23,8 +23,10 @@ namespace tgc {
 // CTA makes the sums over all requests for itself (at most 8192, from L2) and
 // then takes its share of the pages and tokens; no CTA waits for another.
 // Bound by latency: launch, two rounds of loads, one scan.
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
+// Threads of a CTA: about one per request, 128 to 1024 (a decode step of 64 requests
+// spends its time in the barriers, 4096 requests in the loads of the sums).
+constexpr int kPlanMinThreads = 128;
+constexpr int kPlanMaxThreads = 1024;
 
 struct PlanParams {
     const int32_t *lens, *add, *starts, *offsets, *ring;
@@ -59,6 +61,14 @@ __device__ __forceinline__ int32_t saturate(int64_t v)
     return v > 0x7fffffff ? 0x7fffffff : static_cast<int32_t>(v);
 }
 
+// Entry of the ring that lies at `at`, for 0 <= at < 3 cap (a 64-bit remainder
+// takes several hundred cycles).
+__device__ __forceinline__ int64_t in_ring(int64_t at, int64_t cap)
+{
+    if (at >= cap) at -= cap;
+    return at >= cap ? at - cap : at;
+}
+
 // Last index i in [0, n) with a[i] <= v, for ascending a with a[0] <= v.
 __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t v)
 {
@@ -73,17 +83,19 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int32_t v)
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p)
+__global__ void __launch_bounds__(kPlanMaxThreads) cache_plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t smem[];
     const int B = p.batch;
     int32_t *s_grow = smem;             // exclusive prefixes, [B]
     int32_t *s_drop = s_grow + B;
     int32_t *s_start = s_drop + B;      // [B + 1]
-    __shared__ Sums s_warp[kPlanWarps + 1];
+    __shared__ Sums s_warp[kPlanMaxThreads / 32 + 1];
+    __shared__ int s_status;
 
+    const int threads = blockDim.x, warps = threads >> 5;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    const int per = (B + threads - 1) / threads;
     const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
 
     const int64_t head = p.ring[0], count = p.ring[1];
@@ -91,6 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages)
         bad |= TG_PLAN_BAD_RING;
     Sums mine{0, 0, 0};
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         const int64_t len = p.lens[b], after = len + p.add[b];
         if (len < 0 || after < 0) bad |= TG_PLAN_BAD_LENGTH;
@@ -116,26 +129,30 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
         if (lane >= d) incl = incl + o;
     }
     if (lane == 31) s_warp[warp + 1] = incl;
-    if (tid == 0) s_warp[0] = {0, 0, 0};
+    if (tid == 0) {
+        s_warp[0] = {0, 0, 0};
+        s_status = 0;
+    }
     __syncthreads();
     if (warp == 0) {
-        Sums w = lane < kPlanWarps ? s_warp[lane + 1] : Sums{0, 0, 0};
+        Sums w = lane < warps ? s_warp[lane + 1] : Sums{0, 0, 0};
 #pragma unroll
-        for (int d = 1; d < kPlanWarps; d <<= 1) {
+        for (int d = 1; d < 32; d <<= 1) {
             const Sums o = shfl_up(w, d);
             if (lane >= d) w = w + o;
         }
         __syncwarp();
-        if (lane < kPlanWarps) s_warp[lane + 1] = w;
+        if (lane < warps) s_warp[lane + 1] = w;
     }
     __syncthreads();
-    const Sums total = s_warp[kPlanWarps];
+    const Sums total = s_warp[warps];
     if (total.grow > count) bad |= TG_PLAN_NO_PAGES;
     if (count + total.drop > p.num_pages) bad |= TG_PLAN_BAD_RING;
     if (!p.starts && total.toks > p.tokens) bad |= TG_PLAN_BAD_TOKENS;
 
     Sums run = s_warp[warp] + incl;   // exclusive: this thread's own sums taken off again
     run = {run.grow - mine.grow, run.drop - mine.drop, run.toks - mine.toks};
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         const int64_t len = p.lens[b], after = len + p.add[b];
         const int64_t have = pages_of(len < 0 ? 0 : len, p.page_shift);
@@ -151,15 +168,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
         }
     }
     if (B == 0 && tid == 0) s_start[0] = p.starts ? p.starts[0] : 0;
-    // Which bits any thread has seen (the barrier also publishes the prefixes).
-    int status = 0;
-#pragma unroll
-    for (int bit = 1; bit <= TG_PLAN_BAD_RING; bit <<= 1)
-        if (__syncthreads_or(bad & bit)) status |= bit;
+    // Bits that any thread has seen (the barrier also publishes the prefixes).
+    if (bad) atomicOr(&s_status, bad);
+    __syncthreads();
+    const int status = s_status;
     const bool fine = status == 0;
 
-    const int64_t t0 = blockIdx.x * int64_t(kPlanThreads) + tid;
-    const int64_t stride = int64_t(gridDim.x) * kPlanThreads;
+    const int64_t t0 = blockIdx.x * int64_t(threads) + tid;
+    const int64_t stride = int64_t(gridDim.x) * threads;
     for (int64_t b = t0; b < B; b += stride)
         p.lens_out[b] = p.lens[b] + (fine ? p.add[b] : 0);
     if (p.starts_out)
@@ -167,20 +183,21 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     if (t0 == 0) {
         p.status[0] = status;
         p.ring_out[0] =
-            static_cast<int32_t>(fine ? (head + total.grow) % p.num_pages : head);
+            static_cast<int32_t>(fine ? in_ring(head + total.grow, p.num_pages) : head);
         p.ring_out[1] = static_cast<int32_t>(fine ? count - total.grow + total.drop : count);
     }
     if (fine && B > 0) {
         for (int64_t i = t0; i < total.grow; i += stride) {
             const int b = last_at_most(s_grow, B, static_cast<int32_t>(i));
             const int64_t col = pages_of(p.lens[b], p.page_shift) + (i - s_grow[b]);
-            p.tables[b * p.table_stride + col] = p.free_pages[(head + i) % p.num_pages];
+            p.tables[b * p.table_stride + col] = p.free_pages[in_ring(head + i, p.num_pages)];
         }
         for (int64_t i = t0; i < total.drop; i += stride) {
             const int b = last_at_most(s_drop, B, static_cast<int32_t>(i));
             const int64_t col =
                 pages_of(int64_t(p.lens[b]) + p.add[b], p.page_shift) + (i - s_drop[b]);
-            p.free_pages[(head + count + i) % p.num_pages] = p.tables[b * p.table_stride + col];
+            p.free_pages[in_ring(head + count + i, p.num_pages)] =
+                p.tables[b * p.table_stride + col];
         }
     }
     const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
                 const int64_t col = pos >> p.page_shift, have = pages_of(len, p.page_shift);
                 const int64_t page =
                     col < have ? p.tables[b * p.table_stride + col]
-                               : p.free_pages[(head + s_grow[b] + (col - have)) % p.num_pages];
+                               : p.free_pages[in_ring(head + s_grow[b] + (col - have), p.num_pages)];
                 slot = (page << p.page_shift) + (pos & page_mask);
             }
         }
@@ -260,18 +277,31 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteP
 }
 
 // ---------------------------------------------------------------- tg_tree_mask
-// A warp takes a token and walks from it to the root through the request's
-// parents in shared memory; lane w (and w + 32) collects the bits of mask word
-// w.  A parent is below its child, so a walk ends after at most 32 * words
-// steps.  Bound by the latency of the walk's shared-memory loads.
-constexpr int kMaskThreads = 256;
-constexpr int kMaskTokens = 32;      // tokens of one CTA
+// A mask row is its parent's row and one bit more.  Tokens are taken in chunks
+// of 32, a mask word each.  First each chunk by itself, a warp per chunk: by
+// doubling over shuffles every token gets the bits of its ancestors within the
+// chunk and `exit`, the first one before it.  Then, chunk after chunk,
+//   row(i) = row(exit(i)) | own word,   count(i) = count(exit(i)) + bits of it,
+// a thread per token and word.  The words are independent of one another: a CTA
+// has 16 of them, for all tokens of a request.  Bound by latency: a barrier and
+// three dependent shared-memory loads per chunk (a walk along the ancestors of
+// a tree of 1000 tokens some 300 generations deep took 110 us, with eight
+// ancestors a step 20 us).
+constexpr int kMaskThreads = 512;
+constexpr int kMaskWords = 16;       // words of a CTA
+static_assert(kMaskThreads == 32 * kMaskWords, "a thread per token of a chunk and word");
 
 struct MaskParams {
     const int32_t *parents, *starts;
     int32_t *mask, *depth;
-    int tokens, batch, words;
+    int tokens, batch, words, slices;     // slices = ceil(words / kMaskWords)
 };
+
+// Shared memory of a CTA: rows, own words, exits and counts of 32 * words tokens.
+constexpr size_t mask_smem(int64_t words)
+{
+    return static_cast<size_t>(words) * 32 * (kMaskWords + 3) * 4;
+}
 
 __device__ __forceinline__ int clamp_row(int v, int tokens)
 {
@@ -280,17 +310,24 @@ __device__ __forceinline__ int clamp_row(int v, int tokens)
 
 __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const MaskParams p)
 {
-    extern __shared__ int16_t s_up[];    // parent of each token; kBad: not a token of a tree
-    constexpr int16_t kBad = -2;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int W = p.words;
-    const int b = blockIdx.x / W, part = blockIdx.x % W;
+    constexpr int kRoot = -1, kBad = -2;       // parents above a root; of no tree
+    extern __shared__ uint32_t s_rows[];       // [tokens][kMaskWords]
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int W = p.words, room = 32 * W;
+    uint32_t *s_own = s_rows + room * kMaskWords;
+    int *s_exit = reinterpret_cast<int *>(s_own + room);
+    int *s_count = s_exit + room;
+    const int b = blockIdx.x / p.slices, w0 = blockIdx.x % p.slices * kMaskWords;
     if (b == p.batch) {
         // Rows before the first request and behind the last.
+        if (w0 > 0) return;
         const int first = clamp_row(p.starts[0], p.tokens);
         const int last = clamp_row(p.starts[p.batch], p.tokens);
         for (int64_t i = tid; i < p.tokens; i += kMaskThreads) {
-            if (i >= first && i < last) continue;
+            if (i >= first && i < last) {
+                i += (last - 1 - i) / kMaskThreads * kMaskThreads;     // past the requests
+                continue;
+            }
             p.depth[i] = -1;
             for (int w = 0; w < W; ++w) p.mask[i * W + w] = 0;
         }
@@ -298,39 +335,62 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const MaskParam
     }
     const int row0 = clamp_row(p.starts[b], p.tokens);
     const int n = clamp_row(p.starts[b + 1], p.tokens) - row0;
-    const int n_tree = min(n, 32 * W);
-    const int i0 = part * kMaskTokens;
-    // Tokens past the mask's width (the last CTA of the request).
-    if (part == W - 1)
+    const int n_tree = min(n, room);
+    // Tokens past the mask's width.
+    if (w0 == 0)
         for (int64_t i = n_tree + tid; i < n; i += kMaskThreads) {
             p.depth[row0 + i] = -1;
             for (int w = 0; w < W; ++w) p.mask[(row0 + i) * W + w] = 0;
         }
-    const int i1 = min(i0 + kMaskTokens, n_tree);
-    if (i0 >= i1) return;
-    for (int i = tid; i < i1; i += kMaskThreads) {
-        const int u = p.parents[row0 + i];
-        s_up[i] = u >= -1 && u < i ? static_cast<int16_t>(u) : kBad;
+    for (int i = tid; i - lane < n_tree; i += kMaskThreads) {
+        const int base = i - lane;             // the warp's chunk
+        int up = kBad;
+        if (i < n_tree) {
+            const int u = p.parents[row0 + i];
+            up = u >= kRoot && u < i ? u : kBad;
+        }
+        uint32_t own = 1u << lane;
+#pragma unroll
+        for (int r = 0; r < 5; ++r) {
+            const bool in = up >= base;
+            const int src = in ? up - base : lane;
+            const uint32_t bits = __shfl_sync(0xffffffffu, own, src);
+            const int next = __shfl_sync(0xffffffffu, up, src);
+            if (in) {
+                own |= bits;
+                up = next;
+            }
+        }
+        s_own[i] = own;
+        s_exit[i] = up;
     }
     __syncthreads();
-    for (int i = i0 + warp; i < i1; i += kMaskThreads / 32) {
-        uint32_t lo = 0, hi = 0;     // words `lane` and `lane + 32`
-        int depth = -1, a = i;
-        while (a >= 0) {
-            const uint32_t bit = 1u << (a & 31);
-            if ((a >> 5) == lane) lo |= bit;
-            if ((a >> 5) == lane + 32) hi |= bit;
-            ++depth;
-            a = s_up[a];
+    const int tok = tid / kMaskWords, w = w0 + tid % kMaskWords;
+    // Entries of rows past the tree's end are never read by others.
+    int up = s_exit[tok];
+    uint32_t own = s_own[tok];
+    for (int c = 0; 32 * c < n_tree; ++c) {
+        const int i = 32 * c + tok;
+        if (i < n_tree) {
+            const int above = up >= 0 ? s_count[up] : (up == kRoot ? 0 : -1);
+            uint32_t row = 0;
+            if (above >= 0) {
+                if (w == c)
+                    row = own;
+                else if (up >= 0)
+                    row = s_rows[up * kMaskWords + tid % kMaskWords];
+            }
+            const int count = above >= 0 ? above + __popc(own) : -1;
+            s_rows[i * kMaskWords + tid % kMaskWords] = row;
+            if (w == w0) s_count[i] = count;
+            if (w < W) p.mask[static_cast<int64_t>(row0 + i) * W + w] = static_cast<int32_t>(row);
+            if (w == 0) p.depth[row0 + i] = count > 0 ? count - 1 : -1;
         }
-        if (a == kBad) {
-            lo = hi = 0;
-            depth = -1;
+        if (i + 32 < n_tree) {
+            up = s_exit[i + 32];
+            own = s_own[i + 32];
         }
-        int32_t *out = p.mask + int64_t(row0 + i) * W;
-        if (lane < W) out[lane] = static_cast<int32_t>(lo);
-        if (lane + 32 < W) out[lane + 32] = static_cast<int32_t>(hi);
-        if (lane == 0) p.depth[row0 + i] = depth;
+        __syncthreads();
     }
 }
 
@@ -424,8 +484,12 @@ tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch
         cudaGetLastError();
         return TG_ERR_LAUNCH;
     }
-    const int grid = grid_for(tokens > batch ? tokens : batch, tgc::kPlanThreads, num_sms, 1);
-    tgc::cache_plan_kernel<<<grid, tgc::kPlanThreads, smem,
+    int threads = static_cast<int>((batch + 31) / 32 * 32);
+    threads = threads < tgc::kPlanMinThreads   ? tgc::kPlanMinThreads
+              : threads > tgc::kPlanMaxThreads ? tgc::kPlanMaxThreads
+                                               : threads;
+    const int grid = grid_for(tokens > batch ? tokens : batch, threads, num_sms, 1);
+    tgc::cache_plan_kernel<<<grid, threads, smem,
                              static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
 }
@@ -530,9 +594,17 @@ tg_status_t tg_tree_mask(const int32_t *parents, int64_t tokens, const int32_t *
     p.tokens = static_cast<int>(tokens);
     p.batch = static_cast<int>(batch);
     p.words = static_cast<int>(words);
-    const int grid = static_cast<int>(batch * words + 1);
-    tgc::tree_mask_kernel<<<grid, tgc::kMaskThreads, static_cast<size_t>(words) * 64,
-                            static_cast<cudaStream_t>(stream)>>>(p);
+    p.slices = static_cast<int>((words + tgc::kMaskWords - 1) / tgc::kMaskWords);
+    const size_t smem = tgc::mask_smem(words);
+    // More than the default limit of shared memory above 20 words.
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(tgc::tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(tgc::mask_smem(TG_TREE_MAX_WORDS))) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    const int grid = (p.batch + 1) * p.slices;
+    tgc::tree_mask_kernel<<<grid, tgc::kMaskThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
 }
 
