@@ -549,17 +549,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return mbar_wait_bounded(bar, parity, abort_flag, limit, p.error_word,
                                              kErrTreeMma);
                 };
-                // S_i,h = Q K_h^T
-                auto issue_s = [&](int i, int h, int halves) -> bool {
-                    const int t = i & 1, j = two ? i >> 1 : i;
-                    const uint32_t qi = two ? qc + t : qc, qs = qi & 1u;
-                    const uint32_t item = j == 0 ? ic : ic + 2 * j - 1, st = item % NS;
-                    if (h == 0) {
-                        if (i < 2 && (two || i == 0) && !wait(&q_full[qs], (qi >> 1) & 1))
-                            return false;
-                        if ((!two || t == 0) && !wait(&kv_full[st], (item / NS) & 1)) return false;
-                    }
-                    tc_fence_after_sync();
+                auto tile_of = [&](int i) { return two ? i >> 1 : i; };
+                // Ring stages of K_j and V_j; true once they are loaded (the second
+                // group of a pair of query tiles finds them so).
+                auto k_item = [&](int j) { return j == 0 ? ic : ic + 2 * j - 1; };
+                auto v_item = [&](int j) { return j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2; };
+                auto ready = [&](int i, uint32_t item) -> bool {
+                    return (two && (i & 1)) || wait(&kv_full[item % NS], (item / NS) & 1);
+                };
+                auto halves_of = [&](int i) { return walk.halves(walk.k0 + tile_of(i)); };
+                // S_i,h = Q K_h^T, K ready
+                auto issue_s = [&](int i, int h, int halves) {
+                    const int t = i & 1;
+                    const uint32_t qs = (two ? qc + t : qc) & 1u;
+                    const uint32_t st = k_item(tile_of(i)) % NS;
                     const uint64_t qd =
                         smem_desc_sw128(sbase + S::kQOff + qs * S::kTileBytes, 16, 1024);
                     const uint64_t kd = smem_desc_sw128(
@@ -576,49 +579,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!two || t == 1) mma_commit<1>(&kv_empty[st]);
                         if (two ? i + 2 >= N : i + 1 == N) mma_commit<1>(&q_empty[qs]);
                     }
-                    return true;
                 };
-                // O_t += P_i,h V_h
-                auto issue_pv = [&](int i, int h, int halves) -> bool {
-                    const int t = i & 1, j = two ? i >> 1 : i;
-                    const uint32_t item = j == n - 1 ? ic + 2 * n - 1 : ic + 2 * j + 2;
-                    const uint32_t st = item % NS;
-                    if (h == 0) {
-                        if (i == 0 && parts > 0 && !wait(o_free, (parts - 1) & 1)) return false;
-                        if ((!two || t == 0) && !wait(&kv_full[st], (item / NS) & 1)) return false;
-                    }
+                // O_t += P_i,h V_h, V ready
+                auto issue_pv = [&](int i, int h, int halves, uint32_t st, uint64_t vd) -> bool {
+                    const int t = i & 1;
                     const uint32_t pb = 2 * t + h;
-                    if (!wait(&p_full[pb], (p_phase >> pb) & 1)) return false;
-                    p_phase ^= 1u << pb;
-                    tc_fence_after_sync();
-                    const uint64_t vd =
-                        smem_desc_sw128(sbase + S::kKVOff + st * S::kTileBytes + h * kHalfBytes,
-                                        kAtomBytes, 1024);
                     const uint32_t od = tmem_base + kOBase + t * D;
                     const uint32_t pa = tmem_base + t * kKeys + h * kHalf;
                     const uint32_t more = i >= 2 || h > 0;
+                    if (!wait(&p_full[pb], (p_phase >> pb) & 1)) return false;
+                    p_phase ^= 1u << pb;
+                    tc_fence_after_sync();
 #pragma unroll
                     for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_f16_ts(od, pa + kk * 8, vd + kk * (2048 / 16), kIdescO,
-                                   kk > 0 ? 1u : more);
+                        mma_f16_ts(od, pa + kk * 8, vd + (h * kHalfBytes + kk * 2048) / 16,
+                                   kIdescO, kk > 0 ? 1u : more);
                     mma_commit<1>(&pv_done[2 * t + ((pv_next >> t) & 1)]);
                     pv_next ^= 1u << t;
                     if (h + 1 == halves && (!two || t == 1)) mma_commit<1>(&kv_empty[st]);
                     return true;
                 };
-                auto halves_of = [&](int i) { return walk.halves(walk.k0 + (two ? i >> 1 : i)); };
                 bool good = true;
                 for (int i = 0; good && i < 2 && i < N; ++i) {
+                    const uint32_t qi = two ? qc + i : qc;
+                    good = (i > 0 && !two) || wait(&q_full[qi & 1u], (qi >> 1) & 1);
+                    if (good) good = ready(i, k_item(tile_of(i)));
+                    if (!good) break;
+                    tc_fence_after_sync();
                     const int hn = halves_of(i);
-                    for (int h = 0; good && h < hn; ++h) good = issue_s(i, h, hn);
+                    for (int h = 0; h < hn; ++h) issue_s(i, h, hn);
                 }
+                // The previous part's outputs have been read.
+                if (good && parts > 0) good = wait(o_free, (parts - 1) & 1);
+                int hn = halves_of(0);
+                uint32_t st = v_item(0) % NS;
+                if (good) good = ready(0, v_item(0));
                 for (int i = 0; good && i < N; ++i) {
-                    const int hn = halves_of(i), hs = i + 2 < N ? halves_of(i + 2) : 0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (good && h < hn) good = issue_pv(i, h, hn);
-                        if (good && h < hs) good = issue_s(i + 2, h, hs);
+                    // Between a product P V and the scores behind it the tensor core is
+                    // busy: there the next tiles are waited for.
+                    const uint64_t vd =
+                        smem_desc_sw128(sbase + S::kKVOff + st * S::kTileBytes, kAtomBytes, 1024);
+                    const int hs = i + 2 < N ? halves_of(i + 2) : 0;
+                    good = issue_pv(i, 0, hn, st, vd);
+                    if (good && hs > 0) {
+                        good = ready(i, k_item(tile_of(i + 2)));
+                        if (!good) break;
+                        tc_fence_after_sync();
+                        issue_s(i + 2, 0, hs);
                     }
+                    if (good && hn > 1) good = issue_pv(i, 1, hn, st, vd);
+                    if (good && i + 1 < N) {
+                        hn = halves_of(i + 1);
+                        st = v_item(tile_of(i + 1)) % NS;
+                        good = ready(i + 1, v_item(tile_of(i + 1)));
+                    }
+                    if (good && hs > 1) issue_s(i + 2, 1, hs);
                 }
                 ok = good;
             }
