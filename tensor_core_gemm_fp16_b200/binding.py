@@ -167,6 +167,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib._tree_attention_packed.restype = c_int
     lib.tg_tree_attention_workspace_size.argtypes = [i64]
     lib.tg_tree_attention_workspace_size.restype = sz
+    lib._tree_workspace_halves = {d: (lib.tg_tree_attention_workspace_size(d) + 1) // 2
+                                  for d in (64, 128)}
     _lib = lib
     return lib
 
@@ -653,7 +655,7 @@ def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=N
         out = q.new_empty((n, heads, dim))
     os = _rows("out", out, dt, (n, heads, dim), index)
     if workspace is None:
-        workspace = q.new_empty((tg_tree_attention_workspace_size(dim) + 1) // 2)
+        workspace = q.new_empty(load()._tree_workspace_halves.get(dim, 0))
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{index}")
     args = _TREE_ARGS.pack(

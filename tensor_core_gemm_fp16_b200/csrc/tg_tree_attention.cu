@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
                             m = tmax;
                         }
-                        if (done != pv && __any_sync(0xffffffffu, raise)) {
+                        if (done != pv && __any_sync(0xffffffffu, raise && row < rows)) {
                             if (!wait_pv(done - 1)) {
                                 ok = false;
                                 break;
