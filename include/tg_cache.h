@@ -59,7 +59,7 @@ enum {
 enum {
     TG_PLAN_NO_PAGES = 1,       /* the ring holds fewer pages than are needed       */
     TG_PLAN_TABLE_FULL = 2,     /* a request needs more than max_pages table entries */
-    TG_PLAN_BAD_LENGTH = 4,     /* a length is negative, before or after             */
+    TG_PLAN_BAD_LENGTH = 4,     /* a length is negative or past 2^31 - 1             */
     TG_PLAN_BAD_TOKENS = 8,     /* more tokens than `tokens`, or starts not ascending */
     TG_PLAN_BAD_RING = 16       /* head or count out of range, or more pages given
                                    back than the ring has room for                   */
@@ -116,7 +116,8 @@ tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch
  *             skipped.  Slots that are kept are distinct; if two tokens have the same slot,
  *             each 16 bytes of the row come from one of them.
  *   k_cache, v_cache  16-bit [num_pages][page_size][heads][head_dim] with strides page_stride,
- *             slot_stride and cache_head_stride (both caches the same); written
+ *             slot_stride and cache_head_stride (both caches the same); written.  They may
+ *             be interleaved, but no element belongs to both
  *   head_dim  64 or 128
  *
  * Bits are copied, so any 16-bit type will do.  One kernel.

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) cache_plan_kernel(const PlanP
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         const int64_t len = p.lens[b], after = len + p.add[b];
-        if (len < 0 || after < 0) bad |= TG_PLAN_BAD_LENGTH;
+        if (len < 0 || after < 0 || after > 0x7fffffff) bad |= TG_PLAN_BAD_LENGTH;
         const int64_t have = pages_of(len < 0 ? 0 : len, p.page_shift);
         const int64_t want = pages_of(after < 0 ? 0 : after, p.page_shift);
         if (have > p.max_pages || want > p.max_pages) bad |= TG_PLAN_TABLE_FULL;

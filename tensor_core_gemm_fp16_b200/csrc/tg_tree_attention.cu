@@ -127,7 +127,8 @@ struct TreeShape {
     static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
     static constexpr int kFlagOff = kAbortOff + 4;
-    static constexpr int kDynamicBytes = kFlagOff + 4;
+    static constexpr int kItemsOff = kFlagOff + 4;           // ring items of each producer
+    static constexpr int kDynamicBytes = kItemsOff + 4 * kProducers;
     static_assert(kDynamicBytes <= 232448, "shared-memory budget");
     // Floats of one part of a divided unit's query tile: O (by columns), m, l.
     static constexpr int kPartFloats = (D + 2) * kRows;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kTmemSlotOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kAbortOff);
     volatile int *odd_values = reinterpret_cast<volatile int *>(smem + S::kFlagOff);
+    volatile uint32_t *items = reinterpret_cast<volatile uint32_t *>(smem + S::kItemsOff);
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kMlOff);
 
     const int warp = threadIdx.x >> 5;
@@ -326,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = b0; b < b1; ++b) work += request(p, b).work;
     if (threadIdx.x < S::kNumBars) {
         uint64_t *bar = &bars[threadIdx.x];
-        const uint32_t count = (bar >= p_full && bar < pv_done)    ? 4u
+        const uint32_t count = (bar >= kv_full && bar < kv_empty)  ? kProducers
+                               : (bar >= p_full && bar < pv_done)  ? 4u
                                : (bar == o_free || bar == ml_full) ? 8u
                                                                    : 1u;
         mbar_init(bar, count);
@@ -427,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp == kProducerWarp || warp > kMmaWarp) {
-        // Producer `me` of kProducers; the first one also announces the bytes.
+        // Producer `me` of kProducers; each announces the bytes of its own copies,
+        // the first one also those of whole tiles and of the queries.
         const int me = warp == kProducerWarp ? 0 : warp - kMmaWarp;
         uint32_t qc = 0, ic = 0;       // query tiles and ring items so far
         bool ok = true;
@@ -471,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int left = r.ctx - kj * kKeys;
                     const int pages =
                         small ? min(per_tile, (left + (1 << shift) - 1) >> shift) : 1;
-                    const int rows = small ? pages << shift : kKeys;
+                    // rows of this producer's pages
+                    const int rows = small ? (pages - me + kProducers - 1) / kProducers << shift
+                                           : (me == 0 ? kKeys : 0);
                     const int y = small ? 0 : (kj * kKeys) & ((1 << shift) - 1);
                     const CUtensorMap *map = value ? &tmVC : &tmKC;
-                    if (me == 0 && elect_lane())
-                        mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
+                    if (elect_lane()) mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
                     for (int i = me; i < pages; i += kProducers) {
                         const int id = __shfl_sync(0xffffffffu, page, i);
                         if (elect_lane() && !skip)
@@ -484,10 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tma_load_4d(dst + a * kAtomBytes + (i << (shift + 7)), map,
                                             &kv_full[st], a * kAtom, y, walk.head, id);
                     }
-                } else if (me == 0 && elect_lane()) {
-                    mbar_arrive_expect_tx(&kv_full[st], S::kTileBytes);
+                } else if (elect_lane()) {
+                    mbar_arrive_expect_tx(&kv_full[st], me == 0 ? S::kTileBytes : 0);
                     const CUtensorMap *map = value ? &tmV : &tmK;
-                    if (!skip)
+                    if (me == 0 && !skip)
 #pragma unroll
                         for (int a = 0; a < S::kAtoms; ++a)
                             tma_load_3d(dst + a * kAtomBytes, map, &kv_full[st], a * kAtom,
@@ -517,16 +522,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // Every copy lands before shared memory goes away (the injected test
-        // skips one load, whose barrier never completes).
-        if (me == 0 && lane == 0) {
-            for (uint32_t s = 0; s < 2; ++s)
-                if (qc > s && !mbar_wait_drain(&q_full[s], ((qc - 1 - s) >> 1) & 1, limit))
-                    atomicOr(p.error_word, kErrTreeDrain);
-            for (uint32_t s = 0; s < NS; ++s)
-                if (ic > s && !(p.inject == 1 && cta == 0 && s == 0 && ic <= NS) &&
-                    !mbar_wait_drain(&kv_full[s], ((ic - 1 - s) / NS) & 1, limit))
-                    atomicOr(p.error_word, kErrTreeDrain);
+        // Every copy lands before shared memory goes away.  After an expiry the
+        // producers may have stopped at different items: each makes up for those
+        // it has not arrived at, so that all phases that were begun end.  (The
+        // injected test skips one load, whose barrier never completes.)
+        if (lane == 0) items[me] = ic;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kProducers) : "memory");
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < kProducers; ++i) most = max(most, items[i]);
+        if (lane == 0) {
+            for (uint32_t i = ic; i < most; ++i) mbar_arrive(&kv_full[i % NS]);
+            if (me == 0) {
+                for (uint32_t s = 0; s < 2; ++s)
+                    if (qc > s && !mbar_wait_drain(&q_full[s], ((qc - 1 - s) >> 1) & 1, limit))
+                        atomicOr(p.error_word, kErrTreeDrain);
+                for (uint32_t s = 0; s < NS; ++s)
+                    if (most > s && !(p.inject == 1 && cta == 0 && s == 0 && most <= NS) &&
+                        !mbar_wait_drain(&kv_full[s], ((most - 1 - s) / NS) & 1, limit))
+                        atomicOr(p.error_word, kErrTreeDrain);
+            }
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {

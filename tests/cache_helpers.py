@@ -27,7 +27,7 @@ def plan_reference(lens, add, ring, free_pages, tables, page, tokens, starts=Non
         status |= 1
     if any(max(h, w) > width for h, w in zip(have, want)):
         status |= 2
-    if any(n < 0 or n + a < 0 for n, a in zip(lens, add)):
+    if any(n < 0 or not 0 <= n + a < 2 ** 31 for n, a in zip(lens, add)):
         status |= 4
     if starts is None:
         if packing[-1] > tokens:

@@ -159,7 +159,7 @@ def test_plan_refuses_on_the_device_and_changes_nothing(what):
     elif what == "overfull":
         add, tokens, ring, bit = [-16, -33], 0, [0, 5], 16
     elif what == "huge":
-        lens, add, bit = [2 ** 31 - 1, 2 ** 31 - 1], [2 ** 31 - 1, 2 ** 31 - 1], 1 | 2 | 8
+        lens, add, bit = [2 ** 31 - 1, 2 ** 31 - 1], [2 ** 31 - 1, 2 ** 31 - 1], 1 | 2 | 4 | 8
     elif what == "several":
         add, ring, bit = [200, -40], [0, 7], 1 | 2 | 4 | 8 | 16
     if what == "huge":
