@@ -76,6 +76,7 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kWarps = 12;
 constexpr int kProducers = 3;      // warps 8, 10 and 11
+constexpr int kLongPart = 16;      // key tiles of a part whose unused query rows are zeroed
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOBase = 256;
@@ -556,10 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool two = walk.two;
             const int n = walk.k1 - walk.k0;
             const int N = two ? 2 * n : n;
+            // Rows of the query tiles that no token of the request has (what the box
+            // brought of the next request, or an earlier part's) become zero in long
+            // parts: the products with them cost power, and with it clock, for
+            // nothing (64 requests of 16 tokens back to back at the 1000 W limit: 265 us
+            // a call without, 253 with).  In short parts the zeroing costs more than
+            // it gives (parts of 10 tiles: 38.3 us without, 40.6 with).
+            for (int t = 0; ok && n >= kLongPart && t < (two ? 2 : 1); ++t) {
+                const int rows =
+                    min(p.tile_tokens, walk.r.n - (2 * walk.pair + t) * p.tile_tokens) * p.group;
+                if (rows == kRows) continue;
+                const uint32_t qs = (qc + t) & 1u;
+                ok = wait_all(&q_full[qs], ((qc + t) >> 1) & 1, kErrTreeMma);
+                uint8_t *q = smem + S::kQOff + qs * S::kTileBytes;
+                for (int c = rows * 8 + lane; ok && c < kRows * 8; c += 32)
+#pragma unroll
+                    for (int a = 0; a < S::kAtoms; ++a)
+                        *reinterpret_cast<uint4 *>(q + a * kAtomBytes + c * 16) =
+                            make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
             // One thread waits and issues for the whole part.  The tensor core
             // takes few products ahead, so what lies between two of them is kept
             // short: nothing is waited for twice.
-            if (elect_lane()) {
+            if (ok && elect_lane()) {
                 auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
                     return mbar_wait_bounded(bar, parity, abort_flag, limit, p.error_word,
                                              kErrTreeMma);
