@@ -47,6 +47,9 @@ class Problem:
         elif layout == "interleaved":
             c = torch.full((pages, 2, page, heads, dim), NAN, dtype=dtype, device=DEV)
             self.kc, self.vc = c[:, 0], c[:, 1]
+        elif layout == "padded":        # heads 8 elements further apart than they are wide
+            c = torch.full((2, pages, page, heads, dim + 8), NAN, dtype=dtype, device=DEV)
+            self.kc, self.vc = c[0, ..., :dim], c[1, ..., :dim]
         else:
             c = torch.full((2, pages, heads, page, dim), NAN, dtype=dtype, device=DEV)
             self.kc, self.vc = c[0].transpose(1, 2), c[1].transpose(1, 2)
@@ -113,10 +116,12 @@ def test_shapes(shape, dim, dtype):
                 masked=masked, seed=shape, pad=3 if shape % 2 else 0).check(f"masked={masked}")
 
 
-@pytest.mark.parametrize("layout", ["interleaved", "heads_first"])
+@pytest.mark.parametrize("page", [8, 16, 128, 256])
+@pytest.mark.parametrize("layout", ["interleaved", "heads_first", "padded"])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_strided_caches_and_projections(dim, layout):
-    p = Problem([6, 20, 1], [90, 400, 33], heads=3, group=2, dim=dim, layout=layout, seed=3, pad=2)
+def test_strided_caches_and_projections(dim, layout, page):
+    p = Problem([6, 20, 1], [90, 400, 33], heads=3, group=2, dim=dim, layout=layout, seed=3, pad=2,
+                page=page)
     wide = torch.full((p.q.shape[0], p.q.shape[1] + 1, dim + 8), 7.0, dtype=p.dtype, device=DEV)
     p.check(layout, out=wide[:, 1:, :dim])
     assert bool((wide[:, 0] == 7.0).all()) and bool((wide[:, :, dim:] == 7.0).all())
