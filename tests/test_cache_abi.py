@@ -171,3 +171,35 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         binding.tree_mask(i32, i32[:2], 1)
     with pytest.raises(ValueError):
         binding.tree_attention(h, h, h, c, c.clone(), i32.view(4, 1), i32, i32)
+
+
+def test_header_compiles_as_strict_c99(tmp_path):
+    """A C program that uses the header compiles, links and runs its host-only parts."""
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "client.c"
+    src.write_text('''#include <stdio.h>
+#include "tg_cache.h"
+int main(void)
+{
+    tg_tree_attention_t a = {0};
+    a.tokens = -1;
+    printf("%d %d %zu %zu\\n", (int)tg_tree_attention(&a, NULL),
+           (int)tg_tree_mask(NULL, 0, NULL, 0, 1, NULL, NULL, NULL), sizeof a,
+           tg_tree_attention_workspace_size(128));
+    return 0;
+}
+''')
+    libdir = os.path.dirname(binding.LIB_PATH)
+    subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                    os.path.dirname(binding.HEADER), str(src), "-L", libdir, "-ltg_gemm",
+                    f"-Wl,-rpath,{libdir}", "-o", str(tmp_path / "client")], check=True)
+    out = subprocess.run([str(tmp_path / "client")], capture_output=True, text=True, timeout=120)
+    import ctypes
+    want = f"{BAD} {OK} {ctypes.sizeof(binding.tg_tree_attention_t)} " \
+           f"{binding.tg_tree_attention_workspace_size(128)}"
+    assert out.stdout.strip() == want
