@@ -96,8 +96,9 @@ enum {
  *
  * Pages are taken from the head in the order of the requests, and given back in that order
  * behind the tail; pages given back by a call can be taken by the next one.  ring_out and
- * lens_out become ring and lens of the next call.  batch <= TG_CACHE_MAX_BATCH,
- * num_pages >= 1, tokens < 2^31.  One kernel.
+ * lens_out become ring and lens of the next call.  A page belongs to one request: pages that
+ * requests share are the caller's to count, and must not be given back twice.
+ * batch <= TG_CACHE_MAX_BATCH, num_pages >= 1, tokens < 2^31.  One kernel.
  */
 tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch,
                           const int32_t *starts, const int32_t *offsets, int64_t tokens,
