@@ -129,7 +129,8 @@ struct TreeShape {
     static constexpr int kAbortOff = kTmemSlotOff + 4;
     static constexpr int kFlagOff = kAbortOff + 4;
     static constexpr int kItemsOff = kFlagOff + 4;           // ring items of each producer
-    static constexpr int kDynamicBytes = kItemsOff + 4 * kProducers;
+    static constexpr int kIdsOff = kItemsOff + 4 * kProducers;   // page entries, 2 x 32 each
+    static constexpr int kDynamicBytes = kIdsOff + 256 * kProducers;
     static_assert(kDynamicBytes <= 232448, "shared-memory budget");
     // Floats of one part of a divided unit's query tile: O (by columns), m, l.
     static constexpr int kPartFloats = (D + 2) * kRows;
@@ -439,22 +440,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int shift = p.page_shift;
         const bool small = shift < 7;                     // pages of less than a tile
         const int per_tile = small ? kKeys >> shift : 1;  // pages of a tile
+        const int run_shift = small ? shift - 2 : 5;      // log2 of the tiles that 32 pages fill
+        volatile int *ids = reinterpret_cast<volatile int *>(smem + S::kIdsOff) + me * 64;
         while (ok && walk.next(p, lane)) {
             const Request &r = walk.r;
             const int n = walk.k1 - walk.k0;
             const int32_t *table = p.tables + static_cast<int64_t>(walk.b) * p.table_stride;
-            // Lane i: page i of key tile kj of the cache (-1: none).
-            auto page_of = [&](int kj) -> int {
-                if (kj >= r.ctx_tiles || lane >= per_tile) return -1;
-                const int pi = small ? kj * per_tile + lane : (kj * kKeys) >> shift;
-                return (static_cast<int64_t>(pi) << shift) < r.ctx ? table[pi] : -1;
+            // Lane i: page i of the run of tiles that begins with tile j of the part
+            // (-1: none).
+            auto page_of = [&](int j) -> int {
+                const int kj = walk.k0 + j;
+                if (kj >= r.ctx_tiles) return -1;
+                const int64_t pi = small ? static_cast<int64_t>(kj) * per_tile + lane
+                                         : (static_cast<int64_t>(kj + lane) * kKeys) >> shift;
+                return (pi << shift) < r.ctx ? table[pi] : -1;
             };
-            int page_v = -1, page_k = page_of(walk.k0);
-            for (int t = 0; t < (walk.two ? 2 : 1) && ok; ++t, ++qc) {
+            int page = page_of(0);
+            for (int t = 0; me == 0 && t < (walk.two ? 2 : 1) && ok; ++t, ++qc) {
                 const uint32_t slot = qc & 1u;
                 if (qc >= 2) ok = wait_all(&q_empty[slot], ((qc >> 1) - 1) & 1, kErrTreeProducer);
                 if (!ok) break;
-                if (me == 0 && elect_lane()) {
+                if (elect_lane()) {
                     mbar_arrive_expect_tx(&q_full[slot],
                                           p.group * p.tile_tokens * S::kAtoms * 128);
 #pragma unroll
@@ -465,12 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            // One elected thread issues (with coordinates of its own, each lane's
-            // copy would be issued by itself, several times slower).  Page entries
-            // outside the cache read as zeros (out of the map's range).
-            auto load = [&](int kj, int page, bool value) {
+            // Tile j of the part into the next ring stage.  Page entries outside the
+            // cache read as zeros (out of the map's range).
+            auto load = [&](int j, bool value) -> bool {
                 const uint32_t st = ic % NS;
+                if (ic >= NS && !mbar_wait_bounded(&kv_empty[st], (ic / NS - 1) & 1, abort_flag,
+                                                   limit, p.error_word, kErrTreeProducer))
+                    return false;
                 const uint32_t dst = sbase + S::kKVOff + st * S::kTileBytes;
+                const int kj = walk.k0 + j;
                 const bool skip = p.inject == 1 && cta == 0 && ic == 0;
                 if (kj < r.ctx_tiles) {
                     const int left = r.ctx - kj * kKeys;
@@ -481,16 +490,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            : (me == 0 ? kKeys : 0);
                     const int y = small ? 0 : (kj * kKeys) & ((1 << shift) - 1);
                     const CUtensorMap *map = value ? &tmVC : &tmKC;
-                    if (elect_lane()) mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
-                    for (int i = me; i < pages; i += kProducers) {
-                        const int id = __shfl_sync(0xffffffffu, page, i);
-                        if (elect_lane() && !skip)
+                    const int id0 = ((j >> run_shift) & 1) * 32 +
+                                    (j & ((1 << run_shift) - 1)) * per_tile;
+                    mbar_arrive_expect_tx(&kv_full[st], rows * S::kAtoms * 128);
+                    for (int i = me; i < pages && !skip; i += kProducers) {
+                        const int id = ids[id0 + i];
 #pragma unroll
-                            for (int a = 0; a < S::kAtoms; ++a)
-                                tma_load_4d(dst + a * kAtomBytes + (i << (shift + 7)), map,
-                                            &kv_full[st], a * kAtom, y, walk.head, id);
+                        for (int a = 0; a < S::kAtoms; ++a)
+                            tma_load_4d(dst + a * kAtomBytes + (i << (shift + 7)), map,
+                                        &kv_full[st], a * kAtom, y, walk.head, id);
                     }
-                } else if (elect_lane()) {
+                } else {
                     mbar_arrive_expect_tx(&kv_full[st], me == 0 ? S::kTileBytes : 0);
                     const CUtensorMap *map = value ? &tmV : &tmK;
                     if (me == 0 && !skip)
@@ -499,28 +509,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(dst + a * kAtomBytes, map, &kv_full[st], a * kAtom,
                                         r.s0 + (kj - r.ctx_tiles) * kKeys, walk.head);
                 }
-                __syncwarp();
                 ++ic;
+                return true;
             };
-            // Items K_0 | K_1 V_0 | K_2 V_1 | ... | V_n-1; the next tile's page
-            // entries are fetched while the ring has no room.
-            for (int t = 0; t < 2 * n && ok; ++t) {
-                if (ic >= NS)
-                    ok = wait_all(&kv_empty[ic % NS], (ic / NS - 1) & 1, kErrTreeProducer);
-                if (!ok) break;
-                const bool value = t == 2 * n - 1 || (t > 0 && (t & 1) == 0);
-                const int j = t == 2 * n - 1 ? n - 1 : (value ? t / 2 - 1 : (t + 1) / 2);
-                if (value) {
-                    load(walk.k0 + j, page_v, true);
-                    page_v = page_k;
-                    if (j + 2 < n) page_k = page_of(walk.k0 + j + 2);
-                } else {
-                    load(walk.k0 + j, page_k, false);
-                    if (j == 0) {
-                        page_v = page_k;
-                        if (n > 1) page_k = page_of(walk.k0 + 1);
+            // Items K_0 | K_1 V_0 | K_2 V_1 | ... | V_n-1.  The page entries of a run of
+            // tiles go through shared memory, those of the next run are on their way
+            // meanwhile; one elected thread waits and issues for the run.  (With the
+            // entries handed from lane to lane an item took the warp about 1000
+            // cycles: 3.6 TB/s at head width 64, LEAN_TBS so.)
+            for (int j0 = 0; ok && j0 < n; j0 += 1 << run_shift) {
+                ids[((j0 >> run_shift) & 1) * 32 + lane] = page;
+                __syncwarp();
+                const int j1 = min(n, j0 + (1 << run_shift));
+                if (j1 < n) page = page_of(j1);
+                if (elect_lane()) {
+                    for (int j = j0; ok && j < j1; ++j) {
+                        ok = load(j, false);
+                        if (ok && j > 0) ok = load(j - 1, true);
                     }
+                    if (ok && j1 == n) ok = load(n - 1, true);
                 }
+                ok = __all_sync(0xffffffffu, ok);
+                ic = __reduce_max_sync(0xffffffffu, ic);
             }
         }
         // Every copy lands before shared memory goes away.  After an expiry the
