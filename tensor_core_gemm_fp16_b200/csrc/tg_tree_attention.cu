@@ -27,9 +27,9 @@
 //                   one group's exponentials run beside the other's products.
 //   warps 8, 10, 11 TMA producers: queries, and keys and values through one
 //                   ring in the order in which the products need them, each
-//                   a third of a tile's pages (a warp needs about 100 cycles
-//                   per copy; with pages of 16 tokens one alone held the
-//                   stream of 64 requests to 4.0 TB/s, three give 5.4).
+//                   a third of a tile's pages (with pages of 16 tokens one
+//                   alone held the stream of 64 requests to 4.0 TB/s, three
+//                   gave 5.4, and 5.9 with what was made faster since).
 //   warp 9          TMEM allocator and MMA issuer.
 // Step i (a key tile of a query tile) belongs to group t = i mod 2 and has two
 // halves of 64 keys, each with its own score columns.  The issuer's order is
@@ -46,6 +46,15 @@
 // zeroes, in shared memory, the values of rows past the end, and elements
 // that are not finite; what visible drafted tokens lose by that is added
 // back at the end from global memory (a rare path behind a flag).
+//
+// What bounds it.  HBM where a row tile has one or two tiles of rows and the
+// cache is long: 151 us for 872 MB (2 requests over up to 131072 tokens, 27
+// tokens x 4 heads a key head), 211 us for 1238 MB (64 requests, up to 16
+// tokens, up to 8192, pages of 16).  With many rows the tensor core's 64-key
+// products and the softmax, both near 1800 cycles per 128 keys of two groups:
+// 167 us for 139.6 GFLOP (16 requests over 4096, 64 tokens x 8 heads).  With
+// short contexts the latencies of a CTA's start, of a part's end and of the
+// join.  Back to back the large calls run at the power limit, 13 to 20% longer.
 //
 // Every wait is bounded; see tg_attention.cu.
 #include <cuda.h>
@@ -516,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // tiles go through shared memory, those of the next run are on their way
             // meanwhile; one elected thread waits and issues for the run.  (With the
             // entries handed from lane to lane an item took the warp about 1000
-            // cycles: 3.6 TB/s at head width 64, LEAN_TBS so.)
+            // cycles, and 64 requests of one token and 4 heads a key head 227 us; so
+            // 212.)
             for (int j0 = 0; ok && j0 < n; j0 += 1 << run_shift) {
                 ids[((j0 >> run_shift) & 1) * 32 + lane] = page;
                 __syncwarp();
