@@ -246,6 +246,30 @@ def test_nan_in_the_context_reaches_every_row_of_the_request():
     assert bool(torch.isnan(out[:4]).all()) and bool(torch.isfinite(out[4:]).all())
 
 
+@pytest.mark.parametrize("trees,lens", [([6, 3], [40, 300]), ([40], [700])])
+def test_rows_that_are_not_finite_stay_alone(trees, lens):
+    """A NaN query makes its own (token, head) row NaN and no other; an infinite key makes the
+    rows that see it with a score of +inf NaN, and has weight 0 where the score is -inf."""
+    p = Problem(trees, lens, heads=2, group=4, dim=64, seed=23)
+    p.q[2, 3, 7] = NAN
+    p.check()
+    p.q[2, 3, 7] = 0.5
+    page = p.tables[0].long()[33 // 16]
+    p.kc[page, 33 % 16, 1, 5] = INF
+    p.check()
+
+
+def test_a_batch_of_padding_only():
+    p = Problem([0, 0, 0], [40, 0, 300], heads=1, group=2, dim=64, seed=24, pad=5)
+    assert bool((p.run() == 7.0).all())
+
+
+def test_many_idle_requests_and_one_token_at_the_end():
+    B = 5000
+    p = Problem([0] * (B - 1) + [1], [0] * (B - 1) + [77], heads=2, group=2, dim=64, seed=25)
+    p.check()
+
+
 def test_page_entries_out_of_range_read_as_zeros():
     p = Problem([3], [100], heads=1, group=2, dim=64, seed=13, masked=False)
     out = p.run()
