@@ -168,7 +168,7 @@ typedef struct {
     int64_t kv_heads;          /* heads of k, v and the caches */
     int64_t group;             /* query heads per key head, 1 .. 128 */
     int64_t head_dim;          /* 64 or 128 */
-    float scale;               /* factor on the scores, > 0 (at least 1e-30); 0: 1/sqrt(head_dim) */
+    float scale;               /* factor on the scores, 1e-30 .. 1e30; 0: 1/sqrt(head_dim) */
     const void *q;             /* [tokens][kv_heads * group][head_dim] */
     int64_t q_token_stride, q_head_stride;
     const void *k, *v;         /* drafted, [tokens][kv_heads][head_dim] */

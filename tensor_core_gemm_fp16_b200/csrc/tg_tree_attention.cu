@@ -1194,7 +1194,7 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
         a.num_pages < 0 || a.num_pages >= kInt32 || a.max_pages < 0 ||
         a.max_pages >= (kInt32 - 256) >> shift || a.table_stride < a.max_pages ||
         a.table_stride >= kInt32 || !std::isfinite(a.scale) || a.scale < 0.f ||
-        (a.scale != 0.f && a.scale < 1e-30f) ||
+        (a.scale != 0.f && (a.scale < 1e-30f || a.scale > 1e30f)) ||
         (a.inject != 0 && a.inject != TG_INJECT_SKIP_FIRST_LOAD))
         return TG_ERR_INVALID_ARG;
     if (a.mask && (a.words < 1 || a.words > (1 << 26) || a.mask_stride < a.words ||

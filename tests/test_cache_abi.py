@@ -136,7 +136,7 @@ def test_tree_attention_refusals():
     for kw in (dict(type=2), dict(type=-1), dict(tokens=-1), dict(tokens=(1 << 31) - 100),
                dict(batch=-1), dict(kv_heads=-1), dict(group=0), dict(group=129),
                dict(head_dim=96), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(scale=float("inf")), dict(scale=1e-31), dict(page_size=4), dict(page_size=48),
+               dict(scale=float("inf")), dict(scale=1e-31), dict(scale=2e30), dict(page_size=4), dict(page_size=48),
                dict(page_size=512), dict(num_pages=-1), dict(max_pages=-1), dict(table_stride=1),
                dict(max_pages=1 << 28, table_stride=1 << 28), dict(words=0), dict(mask_stride=0),
                dict(inject=2), dict(q=None), dict(k=None), dict(v=None), dict(out=None),
