@@ -156,8 +156,9 @@ tg_status_t tg_tree_mask(const int32_t *parents, int64_t tokens, const int32_t *
  * for every token t of request b, over the lens[b] cached tokens of the request and over its
  * own drafted tokens that the mask shows, with the keys and values of head h / group
  * (group = kv_heads query heads share one).  Scores, maxima and sums are fp32; the probabilities
- * enter the second product in the tensors' type; out is rounded once.  A token that sees
- * nothing gets zeros.  What a token does not see has no influence, not even infinities or
+ * enter the second product in the tensors' type (in fp16, those below 2^-32 of the row's
+ * largest are lost); out is rounded once.  A token that sees nothing gets zeros.
+ * What a token does not see has no influence, not even infinities or
  * NaN there (rejected rows, pages' unused rows).  Rows of out outside every request are left
  * as they are.
  */

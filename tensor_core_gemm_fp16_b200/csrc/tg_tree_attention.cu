@@ -158,6 +158,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
+// Probabilities, and their sum beside them, are held times 2^kLift of
+// 2^(score - m).  In fp16 that is 2^15 at most (m may lag 8 behind), and weights
+// down to 2^-32 of the largest count; without the lift those below 2^-25 would be
+// zero in the product and yet part of the sum (32768 keys of weight 2^-25.2
+// beside two of weight 1, whose values were 0, gave 0 instead of 4.1e-4).  bf16
+// has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+
 // Instruction descriptor bits that select bf16 for A and B.
 template <bool BF16>
 constexpr uint32_t kTypeBits = BF16 ? (1u << 7) | (1u << 10) : 0u;
@@ -741,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 4; ++q)
                 bits[q] = mrow && row < rows && q < p.words ? static_cast<uint32_t>(mrow[q]) : 0u;
             float m = -INFINITY;    // running maximum of the scaled scores, log2 units
-            float l = 0.f;          // running sum of 2^(score - m)
+            float l = 0.f;          // running sum of 2^(score - m + lift)
             for (int i = t; ok && i < N; i += 2) {
                 const int j = two ? i >> 1 : i;
                 const int kj = walk.k0 + j;
@@ -821,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st_32x32b_x32(t_o, o);
                             }
                         }
-                        const float mu = m == -INFINITY ? 0.f : m;
+                        const float mu = m == -INFINITY ? 0.f : m - kLift<BF16>;
                         const uint64_t sl2x2 = f2(sl2, sl2), nmu2 = f2(-mu, -mu);
                         uint64_t ps2[4] = {0, 0, 0, 0};
                         // P takes the first 32 columns of S, two keys per column.

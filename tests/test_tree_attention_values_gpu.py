@@ -1,0 +1,47 @@
+"""The attention of drafted trees where weights are very small or values are not finite."""
+import pytest
+import torch
+
+from attention_helpers import assert_rows, definition, parts
+from test_tree_attention_gpu import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+def check(p, what="", **kw):
+    ref, bound, rows = definition(p.q, p.k, p.v, p.kc, p.vc, p.tables, p.lens, p.starts, p.sees,
+                                  kw.get("scale"))
+    out = p.run(**kw)
+    assert_rows(out, ref, bound, rows, what)
+    return out
+
+
+def set_cached(p, b, pos, cache, head, dim, value):
+    page = int(p.tables[b, pos // p.page])
+    cache[page, pos % p.page, head, dim] = value
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tree", [1, 40])
+def test_many_small_weights_beside_dominant_ones(tree, dim, dtype):
+    """32768 keys of weight 2^-25.2 beside two dominant ones, whose values are 0: the small
+    weights make up the whole output.  148 requests that share one context give each CTA a whole
+    unit, so that small and dominant ones meet under one running maximum."""
+    n, B = 32768, 148
+    p = Problem([tree], [n], heads=1, group=4, dim=dim, page=64, dtype=dtype, masked=False)
+    p.q.zero_()
+    p.q[..., 0] = 1.0
+    for c in (p.k, p.kc):
+        c.nan_to_num_().zero_()
+    for c in (p.v, p.vc):
+        c.nan_to_num_().fill_(1.0)
+    for pos in (5, 200):                        # key tiles 0 and 1: one of either softmax group
+        set_cached(p, 0, pos, p.kc, 0, 0, 17.5)
+        set_cached(p, 0, pos, p.vc, 0, slice(None), 0.0)
+    p.q, p.k, p.v = (x.repeat(B, 1, 1) for x in (p.q, p.k, p.v))
+    p.tables = p.tables.repeat(B, 1)
+    p.lens, p.trees = [n] * B, [tree] * B
+    p.starts = [tree * b for b in range(B + 1)]
+    assert all(len(c) == 1 and c[0][0] == c[0][1] for c in parts(p.trees, p.lens, 1, 4))
+    check(p, scale=1.0)
