@@ -157,10 +157,12 @@ tg_status_t tg_tree_mask(const int32_t *parents, int64_t tokens, const int32_t *
  * own drafted tokens that the mask shows, with the keys and values of head h / group
  * (group = kv_heads query heads share one).  Scores, maxima and sums are fp32; the probabilities
  * enter the second product in the tensors' type (in fp16, those below 2^-32 of the row's
- * largest are lost); out is rounded once.  A token that sees nothing gets zeros.
- * What a token does not see has no influence, not even infinities or
- * NaN there (rejected rows, pages' unused rows).  Rows of out outside every request are left
- * as they are.
+ * largest are lost); out is rounded once.  A token that sees nothing, or nothing with a score
+ * above -inf, gets zeros.  What a token does not see has no influence, not even infinities or
+ * NaN there (rejected rows, pages' unused rows).  An infinite value that it sees makes the
+ * element infinite, or NaN where the key's weight is 0 (a score of -inf); a cached one (not a
+ * drafted one) may also give NaN where its weight is too small for the tensors' type.  Rows of
+ * out outside every request are left as they are.
  */
 typedef struct {
     int type;                  /* TG_TYPE_FP16 or TG_TYPE_BF16, of all tensors */

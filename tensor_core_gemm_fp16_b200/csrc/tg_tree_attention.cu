@@ -107,8 +107,10 @@ struct Split {
 
 struct TreeParams {
     const int32_t *lens, *starts, *tables, *mask;
-    const uint16_t *v;            // drafted values
+    const uint16_t *q, *k, *v;    // queries, drafted keys and values
     uint16_t *out;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
     int64_t v_token_stride, v_head_stride;
     int64_t out_token_stride, out_head_stride;
     int64_t table_stride, max_len, mask_stride;
@@ -201,6 +203,24 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst_smem, const CUtensorMap
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst_smem),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+// An element of a 16-bit tensor.
+template <bool BF16>
+__device__ __forceinline__ float value_of(uint16_t bits)
+{
+    if constexpr (BF16)
+        return __uint_as_float(static_cast<uint32_t>(bits) << 16);
+    else
+        return __half2float(__ushort_as_half(bits));
+}
+
+// True for infinities and NaN: an exponent of all ones.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(uint16_t bits)
+{
+    constexpr uint16_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+    return (bits & kExp) == kExp;
 }
 
 // a / b for a >= 0, b > 0.  A 64-bit division takes several hundred cycles and as
@@ -971,7 +991,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (odd && row < rows) {
                         // Values that are not finite, of drafted tokens that this
-                        // row sees (their weights are positive).
+                        // row sees: a positive weight leaves them what they are,
+                        // and the weight 0 of a score of -inf makes them NaN.
                         const int jlo = max(walk.k0 - r.ctx_tiles, 0) * kKeys;
                         const int jhi = min((walk.k1 - r.ctx_tiles) * kKeys, r.n);
 #pragma unroll 1
@@ -980,20 +1001,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mrow ? (jj >> 5) < p.words && ((mrow[jj >> 5] >> (jj & 31)) & 1)
                                      : jj <= tok;
                             if (!sees) continue;
-                            const uint16_t *vr =
-                                p.v + (static_cast<int64_t>(r.s0) + jj) * p.v_token_stride +
-                                walk.head * p.v_head_stride + c * 32;
+                            const int64_t krow = static_cast<int64_t>(r.s0) + jj;
+                            const uint16_t *vr = p.v + krow * p.v_token_stride +
+                                                 walk.head * p.v_head_stride + c * 32;
+                            bool hit = false;
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) hit |= not_finite<BF16>(vr[e]);
+                            if (!hit) continue;
+                            const uint16_t *qr = p.q + grow * p.q_token_stride +
+                                                 static_cast<int64_t>(walk.head * p.group + hd) *
+                                                     p.q_head_stride;
+                            const uint16_t *kr =
+                                p.k + krow * p.k_token_stride + walk.head * p.k_head_stride;
+                            float score = 0.f;
+#pragma unroll 1
+                            for (int e = 0; e < D; ++e)
+                                score = fmaf(value_of<BF16>(qr[e]), value_of<BF16>(kr[e]), score);
+                            const float odd_weight = sl2 * score == -INFINITY ? 0.f : 1.f;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const uint16_t bits = vr[e];
-                                if constexpr (BF16) {
-                                    if ((bits & 0x7F80u) == 0x7F80u)
-                                        x[e] += __uint_as_float(static_cast<uint32_t>(bits) << 16);
-                                } else {
-                                    if ((bits & 0x7C00u) == 0x7C00u)
-                                        x[e] += __half2float(__ushort_as_half(bits));
-                                }
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (not_finite<BF16>(vr[e]))
+                                    x[e] = fmaf(value_of<BF16>(vr[e]), odd_weight, x[e]);
                         }
                     }
                     if (whole) {
@@ -1032,6 +1060,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         tmem_dealloc<1>(tmem_base, kTmemCols);
     }
+}
+
+// The weight of a partial result with maximum m beside a maximum mn >= m; at least
+// fp32's smallest number where the part saw anything, so that an infinite output
+// stays infinite however small its weight: how a unit is divided must not show.
+__device__ __forceinline__ float part_weight(float m, float mn)
+{
+    return m == -INFINITY ? 0.f : max_nan(ex2(m - mn), 1.401298464e-45f);
 }
 
 // Joins the parts of the units that more than one CTA worked on:
@@ -1078,8 +1114,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __ldcg(part + (col0 + cg * 8 + e) * kRows);
             const float mn = max_nan(m, ms);
-            const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
-            const float w1 = ms == -INFINITY ? 0.f : ex2(ms - mn);
+            const float w0 = part_weight(m, mn);
+            const float w1 = part_weight(ms, mn);
             m = mn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(x[e], w1, acc[e] * w0);
@@ -1097,8 +1133,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
             const int o = (i << (shift + 1)) + tid;
             const float ms = s_part[9][o];
             const float mn = max_nan(m, ms);
-            const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
-            const float w1 = ms == -INFINITY ? 0.f : ex2(ms - mn);
+            const float w0 = part_weight(m, mn);
+            const float w1 = part_weight(ms, mn);
             m = mn;
 #pragma unroll
             for (int e = 0; e < 9; ++e) acc[e] = fmaf(s_part[e][o], w1, acc[e] * w0);
@@ -1310,8 +1346,14 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
     p.starts = a.starts;
     p.tables = a.block_tables;
     p.mask = a.mask;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.k = static_cast<const uint16_t *>(a.k);
     p.v = static_cast<const uint16_t *>(a.v);
     p.out = static_cast<uint16_t *>(a.out);
+    p.q_token_stride = a.q_token_stride;
+    p.q_head_stride = a.q_head_stride;
+    p.k_token_stride = a.kv_token_stride;
+    p.k_head_stride = a.kv_head_stride;
     p.v_token_stride = a.kv_token_stride;
     p.v_head_stride = a.kv_head_stride;
     p.out_token_stride = a.out_token_stride;

@@ -3,7 +3,8 @@ import pytest
 import torch
 
 from attention_helpers import assert_rows, definition, parts
-from test_tree_attention_gpu import Problem
+from cache_helpers import pack_bits
+from test_tree_attention_gpu import DEV, INF, Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,55 @@ def test_many_small_weights_beside_dominant_ones(tree, dim, dtype):
     p.starts = [tree * b for b in range(B + 1)]
     assert all(len(c) == 1 and c[0][0] == c[0][1] for c in parts(p.trees, p.lens, 1, 4))
     check(p, scale=1.0)
+
+
+def replicate(p, B):
+    """The same request B times (sharing its pages)."""
+    n = p.trees[0]
+    p.q, p.k, p.v = (x[:n].repeat(B, 1, 1) for x in (p.q, p.k, p.v))
+    p.mask = p.mask[:n].repeat(B, 1)
+    p.sees = p.sees[:n] * B
+    p.tables = p.tables[:1].repeat(B, 1)
+    p.lens, p.trees, p.starts = p.lens * B, p.trees * B, [n * b for b in range(B + 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("tree", [6, 70, 150])
+def test_infinite_values_of_small_weight(tree, dtype):
+    """A drafted token with an infinite value makes the rows that see it infinite, however small
+    its weight is beside the context's, whether its unit is divided or not."""
+    p = Problem([tree], [1000], heads=2, group=2, dim=64, dtype=dtype, seed=31)
+    p.q[..., 0] = 8.0
+    p.k[..., 0] = 0.0
+    set_cached(p, 0, 100, p.kc, slice(None), 0, 512.0)      # some 512 above all others
+    p.v[2, 0, 5] = INF
+    p.v[tree - 1, 1, 7] = -INF
+    p.sees[tree - 1] = p.sees[tree - 1] | {2}
+    p.mask = pack_bits(p.sees, p.words).to(DEV)
+    assert all(c[0][0] < c[0][1] for c in parts(p.trees, p.lens, 2, 2))
+    out = check(p, "divided")
+    assert bool(torch.isinf(out).any())
+    replicate(p, 296)
+    whole = [n == u for c in parts(p.trees, p.lens, 2, 2) for n, u, _ in c]
+    assert sum(whole) > len(whole) // 2
+    check(p, "many requests")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("tree", [6, 70, 150])
+def test_values_of_keys_with_weight_zero(tree, dtype):
+    """A drafted token whose score is -inf has weight 0: a finite value does not enter, and an
+    infinite one makes the element NaN (0 times infinity)."""
+    p = Problem([tree], [1000], heads=2, group=2, dim=64, dtype=dtype, seed=32)
+    p.q[..., 3] = 1.0
+    p.k[2, 0, 3] = -INF
+    check(p, "finite value")
+    p.v[2, 0, 5] = INF
+    p.v[2, 0, 6] = -INF
+    p.v[1, 0, 9] = INF                                      # of positive weight
+    p.sees[tree - 1] = p.sees[tree - 1] | {1, 2}
+    p.mask = pack_bits(p.sees, p.words).to(DEV)
+    out = check(p, "divided")
+    assert bool(torch.isnan(out).any()) and bool(torch.isinf(out).any())
+    replicate(p, 296)
+    check(p, "many requests")
