@@ -60,7 +60,8 @@ enum {
     TG_PLAN_NO_PAGES = 1,       /* the ring holds fewer pages than are needed       */
     TG_PLAN_TABLE_FULL = 2,     /* a request needs more than max_pages table entries */
     TG_PLAN_BAD_LENGTH = 4,     /* a length is negative or past 2^31 - 1             */
-    TG_PLAN_BAD_TOKENS = 8,     /* more tokens than `tokens`, or starts not ascending */
+    TG_PLAN_BAD_TOKENS = 8,     /* more tokens than `tokens`, starts not ascending, or a
+                                   request appends more than its tokens in the packing */
     TG_PLAN_BAD_RING = 16       /* head or count out of range, or more pages given
                                    back than the ring has room for                   */
 };
@@ -78,8 +79,10 @@ enum {
  *   offsets       int32 [tokens] or NULL (needs starts).  Token t of request b becomes number
  *                                offsets[t] of its appended tokens; outside 0 .. add[b] - 1 it
  *                                is not kept.  NULL: its rank in the packing.  Offsets of a
- *                                request's kept tokens are distinct (else two tokens get one
- *                                slot).
+ *                                request's kept tokens are 0 .. add[b] - 1, each once: this is
+ *                                the caller's to see to (two tokens with one offset get one
+ *                                slot, and a slot whose offset is missing is counted in
+ *                                lens_out and written by nobody).
  *   tokens        number of rows of slots and positions
  *   block_tables  int32 [batch][max_pages], rows table_stride apart; new entries are written,
  *                                all others (also those of dropped pages) left as they are

@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kPlanMaxThreads) cache_plan_kernel(const PlanP
         mine.drop += have > want ? have - want : 0;
         if (p.starts) {
             const int32_t s = p.starts[b], e = p.starts[b + 1];
-            if (s < 0 || e < s || e > p.tokens) bad |= TG_PLAN_BAD_TOKENS;
+            if (s < 0 || e < s || e > p.tokens || p.add[b] > int64_t(e) - s)
+                bad |= TG_PLAN_BAD_TOKENS;
             s_start[b] = s;
             if (b == B - 1) s_start[B] = e;
         } else {
