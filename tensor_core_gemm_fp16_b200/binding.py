@@ -491,6 +491,12 @@ def _rows(name, t, dtype, shape, index):
     return strides
 
 
+def _same_layout(shape, a, b):
+    """Whether strides a and b reach the same elements of ``shape``: those of dimensions with one
+    element reach nothing (torch leaves there what a slice or a view happened to have)."""
+    return a == b or all(x == y for n, x, y in zip(shape, a, b) if n > 1)
+
+
 def _caches(k_cache, v_cache, dtype, index):
     """Check both caches: (pages, page size, heads, dim) tensors of the same shape and strides,
     the last dimension contiguous; returns shape and strides."""
@@ -501,7 +507,7 @@ def _caches(k_cache, v_cache, dtype, index):
         _refuse("k_cache", k_cache, dtype, shape, index)
     if v_cache.dtype is not dtype or v_cache.get_device() != index:
         _refuse("v_cache", v_cache, dtype, shape, index)
-    if v_cache.shape != shape or v_cache.stride() != strides:
+    if v_cache.shape != shape or not _same_layout(shape, v_cache.stride(), strides):
         raise ValueError("k_cache and v_cache must have the same shape and strides")
     if strides[3] != 1:
         raise ValueError("the caches must have a contiguous last dimension")
@@ -583,7 +589,7 @@ def cache_write(k, v, slots, k_cache, v_cache):
     (pages, page, heads, dim), cs = _caches(k_cache, v_cache, dt, index)
     n = k.shape[0] if k.dim() else 0
     ks = _rows("k", k, dt, (n, heads, dim), index)
-    if _rows("v", v, dt, (n, heads, dim), index) != ks:
+    if not _same_layout(v.shape, _rows("v", v, dt, (n, heads, dim), index), ks):
         raise ValueError("k and v must have the same strides")
     _call(torch, index, "tg_cache_write", load().tg_cache_write, k.data_ptr(), v.data_ptr(), n,
           heads, dim, ks[0], ks[1], _vector("slots", slots, torch.int64, n, index),
@@ -642,7 +648,7 @@ def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=N
     n, heads, _ = q.shape
     qs = _rows("q", q, dt, (n, heads, dim), index)
     ks = _rows("k", k, dt, (n, kv_heads, dim), index)
-    if _rows("v", v, dt, (n, kv_heads, dim), index) != ks:
+    if not _same_layout(v.shape, _rows("v", v, dt, (n, kv_heads, dim), index), ks):
         raise ValueError("k and v must have the same strides")
     B, i32 = lens.numel(), torch.int32
     table, stride, max_pages = _table("block_tables", block_tables, i32, B, index)
