@@ -115,7 +115,7 @@ tg_status_t tg_cache_plan(const int32_t *lens, const int32_t *add, int64_t batch
  * tg_cache_write -- k_cache[slots[t]] = k[t] and v_cache[slots[t]] = v[t] for t < tokens.
  *
  *   k, v      16-bit [tokens][heads][head_dim], row strides token_stride and head_stride
- *             (both tensors the same)
+ *             (both tensors the same; tg_cache_write_ex takes v's apart from k's)
  *   slots     int64 [tokens]; a token whose slot is outside 0 .. num_pages * page_size - 1 is
  *             skipped.  Slots that are kept are distinct; if two tokens have the same slot,
  *             each 16 bytes of the row come from one of them.
@@ -131,6 +131,15 @@ tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t
                            const int64_t *slots, void *k_cache, void *v_cache, int64_t num_pages,
                            int64_t page_size, int64_t page_stride, int64_t slot_stride,
                            int64_t cache_head_stride, void *stream);
+
+/* tg_cache_write with strides of their own for k and v (keys that a rotation made, values that
+   are still a slice of the projection). */
+tg_status_t tg_cache_write_ex(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                              const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                              int64_t tokens, int64_t heads, int64_t head_dim,
+                              const int64_t *slots, void *k_cache, void *v_cache,
+                              int64_t num_pages, int64_t page_size, int64_t page_stride,
+                              int64_t slot_stride, int64_t cache_head_stride, void *stream);
 
 /*
  * tg_tree_mask -- ancestor masks and depths of drafted token trees.
@@ -178,7 +187,7 @@ typedef struct {
     const void *q;             /* [tokens][kv_heads * group][head_dim] */
     int64_t q_token_stride, q_head_stride;
     const void *k, *v;         /* drafted, [tokens][kv_heads][head_dim] */
-    int64_t kv_token_stride, kv_head_stride;
+    int64_t kv_token_stride, kv_head_stride;     /* of k, and of v unless own_v_strides */
     const void *k_cache, *v_cache;   /* [num_pages][page_size][kv_heads][head_dim] */
     int64_t num_pages, page_size;    /* page_size a power of two, 8 .. 256 */
     int64_t page_stride, slot_stride, cache_head_stride;
@@ -200,6 +209,8 @@ typedef struct {
                                   by tg_gemm_check_error as TG_ERR_TIMEOUT */
     int inject;                /* 0, or TG_INJECT_SKIP_FIRST_LOAD: the first CTA skips its first
                                   key load, so that a bounded wait expires (tests) */
+    int own_v_strides;         /* nonzero: v has the two strides that follow, not k's */
+    int64_t v_token_stride, v_head_stride;
 } tg_tree_attention_t;
 
 /* Bytes of workspace for a head width (64 or 128; else 0).  Host only. */

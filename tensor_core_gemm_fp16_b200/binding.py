@@ -96,10 +96,11 @@ class tg_tree_attention_t(ctypes.Structure):
          ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64),
          ("out_head_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
          ("workspace_bytes", ctypes.c_size_t), ("wait_limit_ns", ctypes.c_uint64),
-         ("inject", ctypes.c_int)]
+         ("inject", ctypes.c_int), ("own_v_strides", ctypes.c_int),
+         ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
 
 
-# The same struct as bytes: packing it takes a quarter of the time of setting 36 ctypes fields.
+# The same struct as bytes: packing it takes a quarter of the time of setting 39 ctypes fields.
 _TREE_ARGS = struct.Struct("@" + "".join(
     {ctypes.c_int: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P",
      ctypes.c_size_t: "N", ctypes.c_uint64: "Q"}[t] for _, t in tg_tree_attention_t._fields_)
@@ -158,6 +159,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tg_cache_plan.restype = c_int
     lib.tg_cache_write.argtypes = [vp, vp] + [i64] * 5 + [vp, vp, vp] + [i64] * 5 + [vp]
     lib.tg_cache_write.restype = c_int
+    lib.tg_cache_write_ex.argtypes = [vp, i64, i64, vp] + [i64] * 5 + [vp, vp, vp] + [i64] * 5 + \
+        [vp]
+    lib.tg_cache_write_ex.restype = c_int
     lib.tg_tree_mask.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp]
     lib.tg_tree_mask.restype = c_int
     lib.tg_tree_attention.argtypes = [ctypes.POINTER(tg_tree_attention_t), vp]
@@ -424,6 +428,15 @@ def tg_cache_write(k, v, tokens, heads, head_dim, token_stride, head_stride, slo
                                  cache_head_stride, stream)
 
 
+def tg_cache_write_ex(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, tokens,
+                      heads, head_dim, slots, k_cache, v_cache, num_pages, page_size, page_stride,
+                      slot_stride, cache_head_stride, stream=None) -> int:
+    return load().tg_cache_write_ex(k, k_token_stride, k_head_stride, v, v_token_stride,
+                                    v_head_stride, tokens, heads, head_dim, slots, k_cache,
+                                    v_cache, num_pages, page_size, page_stride, slot_stride,
+                                    cache_head_stride, stream)
+
+
 def tg_tree_mask(parents, tokens, starts, batch, words, mask, depth, stream=None) -> int:
     return load().tg_tree_mask(parents, tokens, starts, batch, words, mask, depth, stream)
 
@@ -576,11 +589,11 @@ def cache_plan(lens, add, ring, free_pages, block_tables, page_size, tokens, *, 
 
 
 def cache_write(k, v, slots, k_cache, v_cache):
-    """k_cache[slots] = k, v_cache[slots] = v on the GPU through tg_cache_write.
+    """k_cache[slots] = k, v_cache[slots] = v on the GPU through tg_cache_write_ex.
 
-    k, v: (tokens, heads, D), any 16-bit type, same strides (slices of a fused projection will
-    do); slots: (tokens,) int64, -1 skips a token; caches: (pages, page size, heads, D), D 64 or
-    128, any strides with a contiguous last dimension.  Returns the caches.
+    k, v: (tokens, heads, D), any 16-bit type (slices of a fused projection will do); slots:
+    (tokens,) int64, -1 skips a token; caches: (pages, page size, heads, D), D 64 or 128, any
+    strides (both the same) with a contiguous last dimension.  Returns the caches.
     """
     import torch
     index, dt = _device_index("k", k), k.dtype
@@ -589,10 +602,9 @@ def cache_write(k, v, slots, k_cache, v_cache):
     (pages, page, heads, dim), cs = _caches(k_cache, v_cache, dt, index)
     n = k.shape[0] if k.dim() else 0
     ks = _rows("k", k, dt, (n, heads, dim), index)
-    if not _same_layout(v.shape, _rows("v", v, dt, (n, heads, dim), index), ks):
-        raise ValueError("k and v must have the same strides")
-    _call(torch, index, "tg_cache_write", load().tg_cache_write, k.data_ptr(), v.data_ptr(), n,
-          heads, dim, ks[0], ks[1], _vector("slots", slots, torch.int64, n, index),
+    vs = _rows("v", v, dt, (n, heads, dim), index)
+    _call(torch, index, "tg_cache_write", load().tg_cache_write_ex, k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], n, heads, dim, _vector("slots", slots, torch.int64, n, index),
           k_cache.data_ptr(), v_cache.data_ptr(), pages, page, cs[0], cs[1], cs[2])
     return k_cache, v_cache
 
@@ -648,8 +660,7 @@ def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=N
     n, heads, _ = q.shape
     qs = _rows("q", q, dt, (n, heads, dim), index)
     ks = _rows("k", k, dt, (n, kv_heads, dim), index)
-    if not _same_layout(v.shape, _rows("v", v, dt, (n, kv_heads, dim), index), ks):
-        raise ValueError("k and v must have the same strides")
+    vs = _rows("v", v, dt, (n, kv_heads, dim), index)
     B, i32 = lens.numel(), torch.int32
     table, stride, max_pages = _table("block_tables", block_tables, i32, B, index)
     bits, mask_stride, words = None, 0, 0
@@ -671,6 +682,6 @@ def tree_attention(q, k, v, k_cache, v_cache, block_tables, lens, starts, mask=N
         table, stride, max_pages, _vector("lens", lens, i32, B, index),
         _vector("starts", starts, i32, B + 1, index), bits or 0, words, mask_stride,
         out.data_ptr(), os[0], os[1], workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), wait_limit_ns, inject)
+        workspace.numel() * workspace.element_size(), wait_limit_ns, inject, 1, vs[0], vs[1])
     _call(torch, index, "tg_tree_attention", load()._tree_attention_packed, args)
     return out

@@ -242,7 +242,8 @@ struct WriteParams {
     uint4 *kc, *vc;
     const int64_t *slots;
     int64_t tokens, num_slots;
-    int64_t token_stride, head_stride;                      // in 16-byte pieces
+    int64_t k_token_stride, k_head_stride;                  // in 16-byte pieces
+    int64_t v_token_stride, v_head_stride;                  // in 16-byte pieces
     int64_t page_stride, slot_stride, cache_head_stride;    // in 16-byte pieces
     int page_shift, dim_shift;                              // log2(page size), log2(head_dim / 8)
     int pieces;                                             // 2 * heads * head_dim / 8
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteP
          t += warps) {
         const int64_t slot = p.slots[t];
         if (slot < 0 || slot >= p.num_slots) continue;
-        const int64_t src0 = t * p.token_stride;
+        const uint4 *k = p.k + t * p.k_token_stride, *v = p.v + t * p.v_token_stride;
         const int64_t dst0 = (slot >> p.page_shift) * p.page_stride +
                              (slot & ((int64_t(1) << p.page_shift) - 1)) * p.slot_stride;
         for (int c0 = lane; c0 < p.pieces; c0 += 32 * kWriteUnroll) {
@@ -267,8 +268,9 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const WriteP
                 const int c = c0 + 32 * u;
                 if (c < p.pieces) {
                     const int e = c < half ? c : c - half;
-                    const int64_t off = src0 + (e >> p.dim_shift) * p.head_stride + (e & dmask);
-                    x[u] = __ldg((c < half ? p.k : p.v) + off);
+                    const int64_t head = (e >> p.dim_shift) *
+                                         (c < half ? p.k_head_stride : p.v_head_stride);
+                    x[u] = __ldg((c < half ? k : v) + head + (e & dmask));
                 }
             }
 #pragma unroll
@@ -510,6 +512,18 @@ tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t
                            int64_t page_size, int64_t page_stride, int64_t slot_stride,
                            int64_t cache_head_stride, void *stream)
 {
+    return tg_cache_write_ex(k, token_stride, head_stride, v, token_stride, head_stride, tokens,
+                             heads, head_dim, slots, k_cache, v_cache, num_pages, page_size,
+                             page_stride, slot_stride, cache_head_stride, stream);
+}
+
+tg_status_t tg_cache_write_ex(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                              const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                              int64_t tokens, int64_t heads, int64_t head_dim,
+                              const int64_t *slots, void *k_cache, void *v_cache,
+                              int64_t num_pages, int64_t page_size, int64_t page_stride,
+                              int64_t slot_stride, int64_t cache_head_stride, void *stream)
+{
     const int shift = page_shift_of(page_size);
     if (tokens < 0 || heads < 0 || heads > (1 << 20) || num_pages < 0 || num_pages >= kInt32 ||
         shift < 0 || (head_dim != 64 && head_dim != 128))
@@ -519,7 +533,10 @@ tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t
     if (!k || !v || !slots || !k_cache || !v_cache) return TG_ERR_INVALID_ARG;
     // Strides of dimensions with more than one element.  Rows of a cache may be
     // interleaved with others, not with one another.
-    const Dim src_dims[] = {{tokens, token_stride}, {heads, head_stride}};
+    const Dim src_dims[] = {{tokens, k_token_stride},
+                            {heads, k_head_stride},
+                            {tokens, v_token_stride},
+                            {heads, v_head_stride}};
     const Dim dst_dims[] = {
         {num_pages, page_stride}, {page_size, slot_stride}, {heads, cache_head_stride}};
     for (const Dim &d : src_dims)
@@ -534,12 +551,13 @@ tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t
     if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_cache, 16) ||
         misaligned(v_cache, 16) || misaligned(slots, 8))
         return TG_ERR_MISALIGNED;
-    const size_t src = extent({{tokens, token_stride}, {heads, head_stride}}, head_dim);
+    const size_t k_src = extent({{tokens, k_token_stride}, {heads, k_head_stride}}, head_dim);
+    const size_t v_src = extent({{tokens, v_token_stride}, {heads, v_head_stride}}, head_dim);
     const size_t dst = extent({{num_pages, page_stride},
                                {page_size, slot_stride},
                                {heads, cache_head_stride}},
                               head_dim);
-    const Range in[] = {{k, src}, {v, src}, {slots, 8 * static_cast<size_t>(tokens)}};
+    const Range in[] = {{k, k_src}, {v, v_src}, {slots, 8 * static_cast<size_t>(tokens)}};
     for (const Range &i : in)
         if (overlap(i, {k_cache, dst}) || overlap(i, {v_cache, dst})) return TG_ERR_INVALID_ARG;
     // The two caches may be interleaved (slices of one tensor), not the same.
@@ -558,8 +576,10 @@ tg_status_t tg_cache_write(const void *k, const void *v, int64_t tokens, int64_t
     p.slots = slots;
     p.tokens = tokens;
     p.num_slots = num_pages << shift;
-    p.token_stride = token_stride / 8;
-    p.head_stride = head_stride / 8;
+    p.k_token_stride = k_token_stride / 8;
+    p.k_head_stride = k_head_stride / 8;
+    p.v_token_stride = v_token_stride / 8;
+    p.v_head_stride = v_head_stride / 8;
     p.page_stride = page_stride / 8;
     p.slot_stride = slot_stride / 8;
     p.cache_head_stride = cache_head_stride / 8;

@@ -1257,11 +1257,15 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
     if (cache && (!a.k_cache || !a.v_cache || !a.block_tables)) return TG_ERR_INVALID_ARG;
 
     const int64_t heads = a.kv_heads * a.group, D = a.head_dim;
+    const int64_t v_token_stride = a.own_v_strides ? a.v_token_stride : a.kv_token_stride;
+    const int64_t v_head_stride = a.own_v_strides ? a.v_head_stride : a.kv_head_stride;
     // Strides of dimensions with more than one element.
     const Dim strides[] = {{a.tokens, a.q_token_stride},
                              {heads, a.q_head_stride},
                              {a.tokens, a.kv_token_stride},
                              {a.kv_heads, a.kv_head_stride},
+                             {a.tokens, v_token_stride},
+                             {a.kv_heads, v_head_stride},
                              {a.tokens, a.out_token_stride},
                              {heads, a.out_head_stride},
                              {cache ? a.num_pages : 1, a.page_stride},
@@ -1279,8 +1283,6 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
         misaligned(a.block_tables, 4) || misaligned(a.mask, 4))
         return TG_ERR_MISALIGNED;
 
-    const size_t new_bytes =
-        extent({{a.tokens, a.kv_token_stride}, {a.kv_heads, a.kv_head_stride}}, D);
     const size_t cache_bytes = cache ? extent({{a.num_pages, a.page_stride},
                                                {a.page_size, a.slot_stride},
                                                {a.kv_heads, a.cache_head_stride}},
@@ -1288,8 +1290,8 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
                                      : 0;
     const Range in[] = {
         {a.q, extent({{a.tokens, a.q_token_stride}, {heads, a.q_head_stride}}, D)},
-        {a.k, new_bytes},
-        {a.v, new_bytes},
+        {a.k, extent({{a.tokens, a.kv_token_stride}, {a.kv_heads, a.kv_head_stride}}, D)},
+        {a.v, extent({{a.tokens, v_token_stride}, {a.kv_heads, v_head_stride}}, D)},
         {a.k_cache, cache_bytes},
         {a.v_cache, cache_bytes},
         {a.block_tables,
@@ -1321,10 +1323,11 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
     }
     {
         const int64_t dims[] = {D, a.tokens, a.kv_heads};
-        const int64_t str[] = {a.kv_token_stride, a.kv_head_stride};
+        const int64_t k_str[] = {a.kv_token_stride, a.kv_head_stride};
+        const int64_t v_str[] = {v_token_stride, v_head_stride};
         const uint32_t box[] = {tgt::kAtom, tgt::kKeys, 1};
-        if (!encode_map(encode, &maps.k, a.k, bf16, 3, dims, str, box) ||
-            !encode_map(encode, &maps.v, a.v, bf16, 3, dims, str, box))
+        if (!encode_map(encode, &maps.k, a.k, bf16, 3, dims, k_str, box) ||
+            !encode_map(encode, &maps.v, a.v, bf16, 3, dims, v_str, box))
             return TG_ERR_CUDA;
     }
     if (cache) {
@@ -1354,8 +1357,8 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
     p.q_head_stride = a.q_head_stride;
     p.k_token_stride = a.kv_token_stride;
     p.k_head_stride = a.kv_head_stride;
-    p.v_token_stride = a.kv_token_stride;
-    p.v_head_stride = a.kv_head_stride;
+    p.v_token_stride = v_token_stride;
+    p.v_head_stride = v_head_stride;
     p.out_token_stride = a.out_token_stride;
     p.out_head_stride = a.out_head_stride;
     p.table_stride = a.table_stride;

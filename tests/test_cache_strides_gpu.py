@@ -43,7 +43,8 @@ def check(q, k, v, kc, vc):
     want_k, want_v = kc.clone(), vc.clone()
     want_k.flatten(0, 1)[slots], want_v.flatten(0, 1)[slots] = k, v
     binding.cache_write(k, v, slots, kc, vc)
-    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    for got, want in ((kc, want_k), (vc, want_v)):
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
 @pytest.mark.parametrize("dim", [64, 128])
@@ -64,3 +65,39 @@ def test_strides_of_single_elements_do_not_count(dim):
     vc = torch.randn(2, 16, 1, dim, device=DEV).half()[::2]
     assert kc.stride() != vc.stride()
     check(q, k, v, kc, vc)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("n,heads,dim", [(2, 2, 64), (9, 1, 128), (40, 3, 64), (150, 2, 128)])
+def test_keys_of_their_own_beside_values_of_the_projection(n, heads, dim, dtype):
+    q, k, v, kc, vc = decode(n, heads, dim, 20, dtype=dtype)
+    assert k.stride(0) != v.stride(0)
+    check(q, k, v, kc, vc)
+    check(q, v, k, kc, vc)
+    # heads first
+    check(q, k.transpose(0, 1).contiguous().transpose(0, 1), v, kc, vc)
+
+
+def test_values_that_are_not_finite_with_strides_of_their_own():
+    q, k, v, kc, vc = decode(40, 2, 64, 20)
+    v[3, 1, 5], v[7, 0, 63] = float("inf"), float("nan")
+    k[5, 0, 2] = float("-inf")
+    v[5, 0, 9] = float("inf")
+    check(q, k, v, kc, vc)
+
+
+def test_values_without_strides_are_refused():
+    """Broadcast values: the attention needs rows of their own, the write copies them."""
+    q, k, v, kc, vc = decode(4, 2, 64, 3)
+    args = (kc, vc, i32([[0, 1, 2]]), i32([9]), i32([0, 4]))
+    for x in (v[:1, :1].expand(4, 2, 64), v[:1].expand(4, 2, 64), v[:, :1].expand(4, 2, 64)):
+        with pytest.raises(binding.TgError):
+            binding.tree_attention(q, k, x, *args)
+        with pytest.raises(binding.TgError):
+            binding.tree_attention(q, x, v, *args)
+        slots = torch.tensor([3, 40, -1, 17], device=DEV)
+        binding.cache_write(k, x, slots, kc, vc)
+        for t, s in ((0, 3), (1, 40), (3, 17)):
+            assert torch.equal(vc[s // 16, s % 16], x[t]) and torch.equal(kc[s // 16, s % 16], k[t])
+    with pytest.raises(ValueError):
+        binding.cache_write(k, v.transpose(1, 2).contiguous().transpose(1, 2), slots, kc, vc)
