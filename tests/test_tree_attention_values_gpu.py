@@ -4,7 +4,7 @@ import torch
 
 from attention_helpers import assert_rows, definition, parts
 from cache_helpers import pack_bits
-from test_tree_attention_gpu import DEV, INF, Problem
+from test_tree_attention_gpu import DEV, INF, NAN, Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,22 @@ def test_values_of_keys_with_weight_zero(tree, dtype):
     assert bool(torch.isnan(out).any()) and bool(torch.isinf(out).any())
     replicate(p, 296)
     check(p, "many requests")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("trees,lens", [([6, 3], [40, 300]), ([40], [700]), ([5, 130], [3000, 60])])
+def test_queries_and_keys_that_are_not_finite(trees, lens, dtype):
+    """A NaN query makes its own (token, head) row NaN and no other.  An infinite cached key makes
+    rows with a score of +inf NaN and has weight 0 in those with -inf; so does a drafted one in
+    the rows that see it."""
+    p = Problem(trees, lens, heads=2, group=4, dim=64, dtype=dtype, seed=23)
+    p.q[2, 3, 7] = NAN
+    out = check(p, "query")
+    assert bool(torch.isnan(out[2, 3]).all()) and int(torch.isnan(out).sum()) == 64
+    p.q[2, 3, 7] = 0.5
+    set_cached(p, 0, 33, p.kc, 1, 5, INF)
+    out = check(p, "cached key")
+    nan = torch.isnan(out[:trees[0], 4:]).all(-1)
+    assert torch.equal(nan, p.q[:trees[0], 4:, 5] > 0) and bool(nan.any()) and not bool(nan.all())
+    p.k[1, 0, 9] = -INF
+    check(p, "drafted key")
