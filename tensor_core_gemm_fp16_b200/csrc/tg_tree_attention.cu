@@ -966,7 +966,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float *part = p.part + (static_cast<int64_t>(cta) * 4 + (walk.k0 == 0 ? 2 : 0) +
                                         (two ? t : 0)) *
                                            S::kPartFloats;
-                const bool odd = *odd_values != 0;
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t o[32];
@@ -989,41 +988,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             x[e] = fmaf(__uint_as_float(o[e]), w0, x[e]);
                     }
-                    if (odd && row < rows) {
-                        // Values that are not finite, of drafted tokens that this
-                        // row sees: a positive weight leaves them what they are,
-                        // and the weight 0 of a score of -inf makes them NaN.
-                        const int jlo = max(walk.k0 - r.ctx_tiles, 0) * kKeys;
-                        const int jhi = min((walk.k1 - r.ctx_tiles) * kKeys, r.n);
-#pragma unroll 1
-                        for (int jj = jlo; jj < jhi; ++jj) {
-                            const bool sees =
-                                mrow ? (jj >> 5) < p.words && ((mrow[jj >> 5] >> (jj & 31)) & 1)
-                                     : jj <= tok;
-                            if (!sees) continue;
-                            const int64_t krow = static_cast<int64_t>(r.s0) + jj;
-                            const uint16_t *vr = p.v + krow * p.v_token_stride +
-                                                 walk.head * p.v_head_stride + c * 32;
-                            bool hit = false;
-#pragma unroll 1
-                            for (int e = 0; e < 32; ++e) hit |= not_finite<BF16>(vr[e]);
-                            if (!hit) continue;
-                            const uint16_t *qr = p.q + grow * p.q_token_stride +
-                                                 static_cast<int64_t>(walk.head * p.group + hd) *
-                                                     p.q_head_stride;
-                            const uint16_t *kr =
-                                p.k + krow * p.k_token_stride + walk.head * p.k_head_stride;
-                            float score = 0.f;
-#pragma unroll 1
-                            for (int e = 0; e < D; ++e)
-                                score = fmaf(value_of<BF16>(qr[e]), value_of<BF16>(kr[e]), score);
-                            const float odd_weight = sl2 * score == -INFINITY ? 0.f : 1.f;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (not_finite<BF16>(vr[e]))
-                                    x[e] = fmaf(value_of<BF16>(vr[e]), odd_weight, x[e]);
-                        }
-                    }
                     if (whole) {
                         if (row < rows) {
 #pragma unroll
@@ -1044,6 +1008,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!whole && row < rows && (two || t == 0)) {
                     __stcg(part + D * kRows + row, m);
                     __stcg(part + (D + 1) * kRows + row, l);
+                }
+                if (*odd_values != 0 && row < rows) {
+                    // Values that are not finite, of drafted tokens that this row
+                    // sees, are added to what has just been written: a positive
+                    // weight leaves them what they are, and the weight 0 of a
+                    // score of -inf makes them NaN.
+                    const int jlo = max(walk.k0 - r.ctx_tiles, 0) * kKeys;
+                    const int jhi = min((walk.k1 - r.ctx_tiles) * kKeys, r.n);
+#pragma unroll 1
+                    for (int jj = jlo; jj < jhi; ++jj) {
+                        const bool sees =
+                            mrow ? (jj >> 5) < p.words && ((mrow[jj >> 5] >> (jj & 31)) & 1)
+                                 : jj <= tok;
+                        if (!sees) continue;
+                        const int64_t krow = static_cast<int64_t>(r.s0) + jj;
+                        const uint16_t *vr =
+                            p.v + krow * p.v_token_stride + walk.head * p.v_head_stride;
+                        float odd_weight = -1.f;
+#pragma unroll 1
+                        for (int e = c_lo * 32; e < c_hi * 32; ++e) {
+                            if (!not_finite<BF16>(vr[e])) continue;
+                            if (odd_weight < 0.f) {
+                                const uint16_t *qr =
+                                    p.q + grow * p.q_token_stride +
+                                    static_cast<int64_t>(walk.head * p.group + hd) *
+                                        p.q_head_stride;
+                                const uint16_t *kr =
+                                    p.k + krow * p.k_token_stride + walk.head * p.k_head_stride;
+                                float score = 0.f;
+#pragma unroll 1
+                                for (int i = 0; i < D; ++i)
+                                    score =
+                                        fmaf(value_of<BF16>(qr[i]), value_of<BF16>(kr[i]), score);
+                                odd_weight = sl2 * score == -INFINITY ? 0.f : 1.f;
+                            }
+                            const float v = value_of<BF16>(vr[e]) * odd_weight;
+                            float *pe = part + e * kRows + row;
+                            if (whole)
+                                orow[e] = static_cast<uint16_t>(
+                                    pack2<BF16>(value_of<BF16>(orow[e]) + v, 0.f));
+                            else
+                                __stcg(pe, __ldcg(pe) + v);
+                        }
+                    }
                 }
             }
             // Outputs read: the next part's products may overwrite them.
