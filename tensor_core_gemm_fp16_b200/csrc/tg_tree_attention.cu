@@ -115,7 +115,7 @@ struct TreeParams {
     int64_t out_token_stride, out_head_stride;
     int64_t table_stride, max_len, mask_stride;
     int tokens, batch, kv_heads, group, tile_tokens, words, page_shift;
-    float scale_log2;             // scale * log2(e)
+    float scale_log2, lag;        // scale * log2(e); scores that make 8 of it
     Split *split;                 // [CTAs]
     float *part;                  // [CTAs][first, last part][query tile][D + 2][128]
     int inject;
@@ -160,8 +160,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
-// Probabilities, and their sum beside them, are held times 2^kLift of
-// 2^(score - m).  In fp16 that is 2^15 at most (m may lag 8 behind), and weights
+// Probabilities, and their sum beside them, are 2^((score - m) sl2 + kLift).
+// In fp16 that is 2^15 at most (m may lag 8 log2 units behind), and weights
 // down to 2^-32 of the largest count; without the lift those below 2^-25 would be
 // zero in the product and yet part of the sum (32768 keys of weight 2^-25.2
 // beside two of weight 1, whose values were 0, gave 0 instead of 4.1e-4).  bf16
@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 bits[q] = mrow && row < rows && q < p.words ? static_cast<uint32_t>(mrow[q]) : 0u;
-            float m = -INFINITY;    // running maximum of the scaled scores, log2 units
-            float l = 0.f;          // running sum of 2^(score - m + lift)
+            float m = -INFINITY;    // running maximum of the scores, before the scale
+            float l = 0.f;          // running sum of 2^((score - m) sl2 + lift)
             for (int i = t; ok && i < N; i += 2) {
                 const int j = two ? i >> 1 : i;
                 const int kj = walk.k0 + j;
@@ -823,14 +823,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 4; c < 32; ++c)
                             mx[c & 3] = max3_nan(mx[c & 3], __uint_as_float(s[0][c]),
                                                  __uint_as_float(s[1][c]));
-                        const float tmax =
-                            sl2 * max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
-                        // Lazy rescale: m moves only when a half raises it by more than 8.
+                        const float smax = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+                        // Lazy rescale: m moves only when a half raises it by more than
+                        // 8 log2 units (as a difference: m + lag may round up far from 0).
                         float alpha = 1.f;
-                        const bool raise = !(tmax <= m + 8.f);
+                        const bool raise = !(smax - m <= p.lag) && smax != -INFINITY;
                         if (raise) {
-                            alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
-                            m = tmax;
+                            alpha = m == -INFINITY ? 0.f : ex2((m - smax) * sl2);
+                            m = smax;
                         }
                         if (done != pv && __any_sync(0xffffffffu, raise && row < rows)) {
                             if (!wait_pv(done - 1)) {
@@ -850,8 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st_32x32b_x32(t_o, o);
                             }
                         }
-                        const float mu = m == -INFINITY ? 0.f : m - kLift<BF16>;
-                        const uint64_t sl2x2 = f2(sl2, sl2), nmu2 = f2(-mu, -mu);
+                        // The difference to the maximum first, then the scale: as one
+                        // multiply-add with a rounded product as the maximum, scores
+                        // from 2^27 on overflowed fp16 (wide trees 165.5 us so, 167.5 as
+                        // it is).
+                        const float nm = m == -INFINITY ? 0.f : -m;
+                        const uint64_t nm2 = f2(nm, nm), sl2x2 = f2(sl2, sl2),
+                                       lift2 = f2(kLift<BF16>, kLift<BF16>);
                         uint64_t ps2[4] = {0, 0, 0, 0};
                         // P takes the first 32 columns of S, two keys per column.
 #pragma unroll
@@ -859,9 +864,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t hp[16];
 #pragma unroll
                             for (int c = 0; c < 32; c += 2) {
-                                const uint64_t a2 = ffma2(f2(__uint_as_float(s[q][c]),
+                                const uint64_t d2 = fadd2(f2(__uint_as_float(s[q][c]),
                                                              __uint_as_float(s[q][c + 1])),
-                                                          sl2x2, nmu2);
+                                                          nm2);
+                                const uint64_t a2 = ffma2(d2, sl2x2, lift2);
                                 float a0, a1;
                                 f2split(a2, a0, a1);
                                 const float e0 = ex2(a0), e1 = ex2(a1);
@@ -949,8 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++joins;
                 const float2 a = ml[row], b = ml[kRows + row];
                 m = max_nan(a.x, b.x);
-                w0 = a.x == -INFINITY ? 0.f : ex2(a.x - m);
-                w1 = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+                w0 = a.x == -INFINITY ? 0.f : ex2((a.x - m) * sl2);
+                w1 = b.x == -INFINITY ? 0.f : ex2((b.x - m) * sl2);
                 l = fmaf(a.y, w0, b.y * w1);
             }
             ++parts;
@@ -1006,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!whole && row < rows && (two || t == 0)) {
-                    __stcg(part + D * kRows + row, m);
+                    __stcg(part + D * kRows + row, m * sl2);      // log2 units from here on
                     __stcg(part + (D + 1) * kRows + row, l);
                 }
                 if (*odd_values != 0 && row < rows) {
@@ -1079,7 +1085,8 @@ __device__ __forceinline__ float part_weight(float m, float mn)
 }
 
 // Joins the parts of the units that more than one CTA worked on:
-//   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s.
+//   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s,
+// with maxima in log2 units.
 // Block (c, y): the unit that began in CTA c's share, 16 columns of one of its
 // query tiles.  A thread has 8 columns of a row for one of `groups` runs of
 // parts, in one pass with a running maximum: rp (a power of two that covers the
@@ -1381,6 +1388,7 @@ tg_status_t tree_attention_impl(const tg_tree_attention_t &a, cudaStream_t strea
     p.page_shift = shift;
     const float scale = a.scale != 0.f ? a.scale : 1.0f / std::sqrt(static_cast<float>(D));
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.lag = 8.0f / p.scale_log2;
     p.split = static_cast<tgt::Split *>(a.workspace);
     p.part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + tgt::split_bytes());
     p.inject = a.inject;
