@@ -26,9 +26,11 @@
  * owned by the caller; asynchronous calls on `stream`; arguments checked on
  * the host before anything is launched (TG_ERR_INVALID_ARG,
  * TG_ERR_MISALIGNED); an output may not overlap an input.  The library
- * allocates nothing here and keeps no pointer.  Values that only the device
- * knows (lengths, pages, slots, parents) are checked there: what lies out of
- * range is skipped as each entry says, and never read or written through.
+ * allocates nothing here and keeps no pointer; the first call on a device sets it up (its
+ * number of SMs, addresses), which may happen inside a stream capture.  Values
+ * that only the device knows (lengths, pages, slots, parents) are checked there:
+ * what lies out of range is skipped as each entry says, and never read or
+ * written through.
  * int32 and int64 arrays are aligned to their element, fp16 / bf16 tensors to
  * 16 bytes, with strides in elements, multiples of 8, and the head dimension
  * contiguous.

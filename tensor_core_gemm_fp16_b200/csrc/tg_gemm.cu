@@ -352,6 +352,18 @@ tg_status_t streamk_workspace(int num_sms, cudaStream_t stream, float **partials
     return TG_OK;
 }
 
+// While one of these lives, this thread may make calls that look up addresses, load
+// modules or create pools although a stream of the process is being captured: the
+// set-up of a device may happen in the first call inside a capture.  None of its
+// calls enters the captured graph.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// One-time set-up per device.  A set-up that failed is tried again by the next call,
+// unless the device is of another kind.
 tg_status_t device_state(DeviceState **out, int *dev_out)
 {
     int dev = -1;
@@ -362,7 +374,8 @@ tg_status_t device_state(DeviceState **out, int *dev_out)
     std::lock_guard<std::mutex> lock(g_mutex);
     DeviceState &d = g_devices[dev];
     if (!d.init) {
-        d.init = true;
+        d.status = TG_OK;
+        const RelaxedCapture relaxed;
         int major = 0, minor = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
@@ -382,7 +395,7 @@ tg_status_t device_state(DeviceState **out, int *dev_out)
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;
             props.location.id = dev;
-            if (cudaMemPoolCreate(&d.pool, &props) != cudaSuccess) {
+            if (!d.pool && cudaMemPoolCreate(&d.pool, &props) != cudaSuccess) {
                 d.pool = nullptr;
                 d.status = TG_ERR_CUDA;
             } else {
@@ -401,6 +414,7 @@ tg_status_t device_state(DeviceState **out, int *dev_out)
                 g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
         }
         cudaGetLastError();
+        d.init = d.status == TG_OK || d.status == TG_ERR_UNSUPPORTED_DEVICE;
     }
     *out = &d;
     if (dev_out) *dev_out = dev;
