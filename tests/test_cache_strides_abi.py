@@ -41,3 +41,13 @@ def test_tree_attention_with_strides_of_the_values(own):
     for kw in (dict(v_token_stride=132), dict(v_head_stride=68)):
         assert call(**kw) == MIS, kw
     assert attend(v_token_stride=0, v_head_stride=3) == NO_DEVICE          # k's strides count
+
+
+def test_packed_struct_matches_the_declared_one():
+    """The bytes that the binding packs are the struct's, field by field."""
+    import ctypes
+    fields = binding.tg_tree_attention_t._fields_
+    assert binding._TREE_ARGS.size == ctypes.sizeof(binding.tg_tree_attention_t)
+    values = list(range(1, len(fields) + 1))
+    s = binding.tg_tree_attention_t.from_buffer_copy(binding._TREE_ARGS.pack(*values))
+    assert [getattr(s, name) for name, _ in fields] == values
