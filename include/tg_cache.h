@@ -200,7 +200,9 @@ typedef struct {
     const int32_t *starts;     /* [batch + 1] packing, clamped to 0 .. tokens */
     const int32_t *mask;       /* [tokens][words], rows mask_stride apart, as tg_tree_mask writes
                                   them; drafted tokens past 32 * words are not seen.  NULL: a
-                                  token sees those of its request up to itself */
+                                  token sees those of its request up to itself (a prompt; key
+                                  tiles above the diagonal are computed and masked, so long
+                                  prompts take about twice the products of the definition) */
     int64_t words, mask_stride;
     void *out;                 /* [tokens][kv_heads * group][head_dim], written */
     int64_t out_token_stride, out_head_stride;

@@ -45,16 +45,22 @@
 // finite there would spread: in a tile that is not wholly visible the group
 // zeroes, in shared memory, the values of rows past the end, and elements
 // that are not finite; what visible drafted tokens lose by that is added
-// back at the end from global memory (a rare path behind a flag).
+// back to the written output from global memory (a rare path behind a flag).
 //
-// What bounds it.  HBM where a row tile has one or two tiles of rows and the
-// cache is long: 151 us for 872 MB (2 requests over up to 131072 tokens, 27
-// tokens x 4 heads a key head), 211 us for 1238 MB (64 requests, up to 16
+// Without a mask a token sees its request's drafted tokens up to itself, but a
+// unit's length does not depend on its query tiles: tiles above the diagonal are
+// computed and masked, so a long prompt takes about twice the products of its
+// definition (2048 tokens of 32 heads 104 us, floor 21).
+//
+// What bounds it (bursts from a captured graph; then back to back, at the power
+// limit).  HBM where a key head has one or two tiles of rows and the cache is
+// long: 151 and 170 us for 872 MB (2 requests over up to 131072 tokens, 27 tokens
+// x 4 heads a key head), 213 and 249 us for 1238 MB (64 requests, up to 16
 // tokens, up to 8192, pages of 16).  With many rows the tensor core's 64-key
-// products and the softmax, both near 1800 cycles per 128 keys of two groups:
-// 167 us for 139.6 GFLOP (16 requests over 4096, 64 tokens x 8 heads).  With
-// short contexts the latencies of a CTA's start, of a part's end and of the
-// join.  Back to back the large calls run at the power limit, 13 to 20% longer.
+// products and the softmax, both near 1800 cycles per 64 keys of both groups:
+// 169 and 200 us for 139.6 GFLOP (16 requests over 4096, 64 tokens x 8 heads),
+// where these products are 206,000 of an SM's 254,000 active cycles.  With short
+// contexts the latencies of a CTA's start, of a part's end and of the join.
 //
 // Every wait is bounded; see tg_attention.cu.
 #include <cuda.h>
@@ -554,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // tiles go through shared memory, those of the next run are on their way
             // meanwhile; one elected thread waits and issues for the run.  (With the
             // entries handed from lane to lane an item took the warp about 1000
-            // cycles, and 64 requests of one token and 4 heads a key head 227 us; so
-            // 212.)
+            // cycles, and 64 requests of one token and 4 heads a key head 227 us in
+            // bursts; so 211.)
             for (int j0 = 0; ok && j0 < n; j0 += 1 << run_shift) {
                 ids[((j0 >> run_shift) & 1) * 32 + lane] = page;
                 __syncwarp();
@@ -609,9 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Rows of the query tiles that no token of the request has (what the box
             // brought of the next request, or an earlier part's) become zero in long
             // parts: the products with them cost power, and with it clock, for
-            // nothing (64 requests of 16 tokens back to back at the 1000 W limit: 265 us
-            // a call without, 253 with).  In short parts the zeroing costs more than
-            // it gives (parts of 10 tiles: 38.3 us without, 40.6 with).
+            // nothing.  Without and with it, back to back at the 1000 W limit: 64 requests
+            // of 16 tokens 256 and 246 us a call (bursts 218 and 212), of 4 tokens 234 and
+            // 224, 16 requests over 8192 (head width 128) 125 and 124, two long trees
+            // 168 and 169 (bursts 151 both).  The limit of 16 tiles is not sharp: with
+            // parts of 10 tiles zeroing took 38.3 to 40.6 us when it was measured there,
+            // and zeroing in all parts gains 0 to 1.5% in the cases above.
             for (int t = 0; ok && n >= kLongPart && t < (two ? 2 : 1); ++t) {
                 const int rows =
                     min(p.tile_tokens, walk.r.n - (2 * walk.pair + t) * p.tile_tokens) * p.group;
