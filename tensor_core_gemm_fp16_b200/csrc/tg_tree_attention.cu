@@ -1021,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!whole && row < rows && (two || t == 0)) {
-                    __stcg(part + D * kRows + row, m * sl2);      // log2 units from here on
+                    __stcg(part + D * kRows + row, m);
                     __stcg(part + (D + 1) * kRows + row, l);
                 }
                 if (*odd_values != 0 && row < rows) {
@@ -1088,26 +1088,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The weight of a partial result with maximum m beside a maximum mn >= m; at least
 // fp32's smallest number where the part saw anything, so that an infinite output
 // stays infinite however small its weight: how a unit is divided must not show.
-__device__ __forceinline__ float part_weight(float m, float mn)
+__device__ __forceinline__ float part_weight(float m, float mn, float sl2)
 {
-    return m == -INFINITY ? 0.f : max_nan(ex2(m - mn), 1.401298464e-45f);
+    return m == -INFINITY ? 0.f : max_nan(ex2((m - mn) * sl2), 1.401298464e-45f);
 }
 
 // Joins the parts of the units that more than one CTA worked on:
-//   O = sum_s O_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s,
-// with maxima in log2 units.
+//   O = sum_s O_s w_s / sum_s l_s w_s,  w_s = 2^((m_s - m) sl2),  m = max_s m_s.
 // Block (c, y): the unit that began in CTA c's share, 16 columns of one of its
 // query tiles.  A thread has 8 columns of a row for one of `groups` runs of
 // parts, in one pass with a running maximum: rp (a power of two that covers the
 // rows in use) x 2 x groups threads.  The groups are then joined in order
 // through shared memory.  Bound by the latency of the partial results' loads
 // (they lie in L2), hence the single pass, and the many groups where there are
-// few rows.
+// few rows.  Five blocks to an SM (48 registers): with four, units of 74 parts took
+// 2.5 us longer.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCols = 16;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p)
+__global__ void __launch_bounds__(kJoinThreads, 5) tree_join_kernel(const TreeParams p)
 {
     using S = TreeShape<D>;
     __shared__ float s_part[10][kJoinThreads];      // 8 columns, maximum and sum
@@ -1123,6 +1123,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
     const int groups = kJoinThreads >> (shift + 1);
     const int per = (ctas + groups - 1) / groups;
     const int s0 = min(g * per, ctas), s1 = min(s0 + per, ctas);
+    const float sl2 = p.scale_log2;
     float m = -INFINITY, acc[9];
 #pragma unroll
     for (int e = 0; e < 9; ++e) acc[e] = 0.f;
@@ -1138,8 +1139,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __ldcg(part + (col0 + cg * 8 + e) * kRows);
             const float mn = max_nan(m, ms);
-            const float w0 = part_weight(m, mn);
-            const float w1 = part_weight(ms, mn);
+            const float w0 = part_weight(m, mn, sl2);
+            const float w1 = part_weight(ms, mn, sl2);
             m = mn;
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(x[e], w1, acc[e] * w0);
@@ -1157,8 +1158,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
             const int o = (i << (shift + 1)) + tid;
             const float ms = s_part[9][o];
             const float mn = max_nan(m, ms);
-            const float w0 = part_weight(m, mn);
-            const float w1 = part_weight(ms, mn);
+            const float w0 = part_weight(m, mn, sl2);
+            const float w1 = part_weight(ms, mn, sl2);
             m = mn;
 #pragma unroll
             for (int e = 0; e < 9; ++e) acc[e] = fmaf(s_part[e][o], w1, acc[e] * w0);

@@ -1,4 +1,6 @@
 """The attention of drafted trees where weights are very small or values are not finite."""
+import math
+
 import pytest
 import torch
 
@@ -189,3 +191,31 @@ def test_far_scores_one_step_of_32_bits_apart(tree, dtype):
         total = 2 + (n - 2 + t + 1) * small
         for e, want in ((0, (n - 2) * small / total), (1, 2 / total), (2, 0.0)):
             assert bool(((out[:, t, :, e] - want).abs() <= (2 * u + 2.0 ** -16) * want).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("scale,log_a,step", [(1.0, 13, 8.0), (2.0 ** -20, 13, 8.0),
+                                              (2.0 ** 99, 15, 128.0)])
+def test_far_scores_in_a_divided_unit(scale, log_a, step, dtype):
+    """One request whose key tiles lie in as many CTAs: parts with neighbouring maxima of 2^26 and
+    2^26 + 8 (or 2^30 and 2^30 + 128, beyond 32 bits after a scale of 2^99) are joined by their
+    distance."""
+    n = 3000
+    p = Problem([1], [n], heads=1, group=4, dim=64, page=16, dtype=dtype, masked=False)
+    p.q.zero_()
+    p.q[..., 0], p.q[..., 1] = 2.0 ** log_a, 1.0
+    for c in (p.k, p.v, p.kc, p.vc):
+        c.nan_to_num_().zero_()
+    p.k[..., 0] = p.kc[..., 0] = 2.0 ** log_a
+    p.vc[..., 0] = 1.0
+    for pos in (1300, 2500):
+        set_cached(p, 0, pos, p.kc, 0, 1, step)
+        set_cached(p, 0, pos, p.vc, 0, 0, 0.0)
+        set_cached(p, 0, pos, p.vc, 0, 1, 1.0)
+    assert all(len(c) == 1 and c[0][0] == 1 for c in parts(p.trees, p.lens, 1, 4))
+    out = p.run(scale=scale)[0].double()
+    u = torch.finfo(dtype).eps / 2
+    small = math.exp(-step * scale)
+    total = 2 + (n - 2 + 1) * small
+    for e, want in ((0, (n - 2) * small / total), (1, 2 / total), (2, 0.0)):
+        assert bool(((out[:, e] - want).abs() <= (2 * u + 2.0 ** -16) * want).all()), (e, want)
